@@ -276,6 +276,128 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
                                    float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* Norms of query and key heads with the rotation by position, in one pass: the
+ * step between a layer's projection and its attention (Qwen3 has the norms,
+ * Llama-3.1 only the rotation).  For each row x of head_dim channels at position p:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (y = x where the weight is NULL)
+ *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a),  a = p * inv_freq[i], i < 64
+ * with j = i + 64, or with channels (2i, 2i+1) when `interleaved` is not 0.  The
+ * product p * inv_freq is taken exactly (positions far beyond 2^24 keep their angle),
+ * the rest in fp32, and a row is rounded once, when it is stored.
+ *
+ *   q        bf16, logical [B, N, Hq, 128]: element strides q_strides between sequences,
+ *            tokens and heads (multiples of 8, not negative); the channels of a row are
+ *            adjacent.  k likewise with Hkv heads.  Views into a packed projection
+ *            output are the usual case.
+ *   positions int32 [B, N] (any value); inv_freq fp32 [64]
+ *   q_weight, k_weight  bf16 [128] or NULL each
+ *   eps      finite, >= 0
+ *   q_out, k_out  like q and k with their own strides, at least 128 where the dimension
+ *            is longer than 1: strides {Hq*N*128, 128, N*128} give the [B, Hq, N, 128] that
+ *            the prefill calls read, and with N = 1 the [B, Hq, 128] of the decode calls.
+ *            An output may be its own input (same pointer and strides); other overlap is
+ *            not allowed.
+ * Any Hq and Hkv (at most 4096) is taken here; B·N <= 2^30. */
+typedef struct {
+  int64_t b, n, h; /* element strides between sequences, tokens, heads */
+} kascade_strides;
+int kascade_qk_norm_rope(kascade_shape s, int32_t N, const uint16_t* q, kascade_strides q_strides,
+                         const uint16_t* k, kascade_strides k_strides, const int32_t* positions,
+                         const float* inv_freq, const uint16_t* q_weight, const uint16_t* k_weight,
+                         float eps, int32_t interleaved, uint16_t* q_out,
+                         kascade_strides q_out_strides, uint16_t* k_out,
+                         kascade_strides k_out_strides, void* stream);
+int kascade_qk_norm_rope_f16(kascade_shape s, int32_t N, const uint16_t* q,
+                             kascade_strides q_strides, const uint16_t* k,
+                             kascade_strides k_strides, const int32_t* positions,
+                             const float* inv_freq, const uint16_t* q_weight,
+                             const uint16_t* k_weight, float eps, int32_t interleaved,
+                             uint16_t* q_out, kascade_strides q_out_strides, uint16_t* k_out,
+                             kascade_strides k_out_strides, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Paged KV cache held in 4 bits: 160 bytes per token and key head instead of 512.
+ *
+ * kv_pages is uint8 [num_pages, Hkv, page_size, KASCADE_Q4_ROW_BYTES], 16-byte aligned; block_table
+ * and page_size are as for the 16-bit paged calls.  A row holds one token of one key
+ * head, K and V:
+ *   bytes   0 ..  63  K codes: channel c is nibble 8*(4*((c>>3)&3) + (c>>5)) + (c&7)
+ *   bytes  64 .. 127  V codes: channel c is nibble 8*(2*((c>>2)&7) + (c>>6)) + 4*((c>>5)&1) + (c&3)
+ *   bytes 128 .. 159  bf16 [4][4]: K scales, K minima, V scales, V minima, one per group of
+ *                     32 channels (nibble i is bits 4(i&1) .. of byte i>>1)
+ * and stands for the values  minimum + scale * code.
+ *
+ * kascade_kv_write_paged_q4 quantises new rows: token n < count[b] of sequence b becomes its
+ * token start[b] + n.  Per group, with all roundings those of exact arithmetic:
+ *   minimum = the largest bf16 <= min(x);  scale = the smallest bf16 >= (max(x) - minimum) / 15
+ *   code = (x - minimum) / scale to the nearest whole number, half to even (0 if scale = 0)
+ * so no value clips and |value - x| <= scale/2.
+ *   k, v     bf16, logical [B, N, Hkv, 128] with element strides as in kascade_qk_norm_rope
+ *   start    int32 [B]; count int32 [B] or NULL (N tokens of every sequence)
+ * kascade_kv_read_paged_q4 is the way back: tokens start[b] .. start[b] + count[b] - 1 into
+ *   k, v     bf16 [B, Hkv, N, 128]; rows at n >= count[b] are left untouched
+ * rounding each value once.
+ *
+ * Sequences whose start or count is negative, whose count exceeds N, or that would end past
+ * max_pages * page_size or 2^30, and tokens whose block-table entry is out of range, are
+ * skipped (KASCADE_ERR_BAD_INDEX in the device status).  A group that holds a NaN or an
+ * infinity, or whose range exceeds the largest float, is stored as scale 0, minimum NaN, reads
+ * back as NaN and sets KASCADE_ERR_NONFINITE.  Two tokens of one call must not share a slot.
+ * s.Hq is not used; B·N <= 2^30, Hkv <= 4096.  The _f16 variants take fp16 rows; the pages
+ * are the same. */
+#define KASCADE_Q4_ROW_BYTES 160
+int kascade_kv_write_paged_q4(kascade_shape s, int32_t N, const uint16_t* k,
+                              kascade_strides k_strides, const uint16_t* v,
+                              kascade_strides v_strides, uint8_t* kv_pages, int32_t num_pages,
+                              const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                              const int32_t* start, const int32_t* count, void* stream);
+int kascade_kv_write_paged_q4_f16(kascade_shape s, int32_t N, const uint16_t* k,
+                                  kascade_strides k_strides, const uint16_t* v,
+                                  kascade_strides v_strides, uint8_t* kv_pages, int32_t num_pages,
+                                  const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                  const int32_t* start, const int32_t* count, void* stream);
+int kascade_kv_read_paged_q4(kascade_shape s, int32_t N, const uint8_t* kv_pages,
+                             int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                             int32_t page_size, const int32_t* start, const int32_t* count,
+                             uint16_t* k, uint16_t* v, void* stream);
+int kascade_kv_read_paged_q4_f16(kascade_shape s, int32_t N, const uint8_t* kv_pages,
+                                 int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                                 int32_t page_size, const int32_t* start, const int32_t* count,
+                                 uint16_t* k, uint16_t* v, void* stream);
+
+/* The two decode calls over 4-bit pages: the same operations, outputs, host checks and
+ * device-side errors as kascade_decode_anchor_paged and kascade_decode_reuse_paged, on the
+ * values the rows stand for.  Logits, softmax statistics and sums are fp32.  A token whose
+ * block-table entry is out of range gets pooled = 0.  A row that stands for NaN makes its own
+ * head group's results NaN.  The reuse call needs no scratch; pooled may be NULL when
+ * max_T = 0, and idx when k_max = 0. */
+size_t kascade_decode_anchor_paged_q4_workspace_bytes(kascade_shape s, int32_t max_T);
+int kascade_decode_anchor_paged_q4(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                   int32_t num_pages, const int32_t* block_table,
+                                   int32_t max_pages, int32_t page_size, const int32_t* seq_len,
+                                   int32_t max_T, float scale, uint16_t* out, float* lse,
+                                   float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes,
+                                   void* stream);
+int kascade_decode_anchor_paged_q4_f16(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                       int32_t num_pages, const int32_t* block_table,
+                                       int32_t max_pages, int32_t page_size,
+                                       const int32_t* seq_len, int32_t max_T, float scale,
+                                       uint16_t* out, float* lse, float* pooled,
+                                       int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream);
+int kascade_decode_reuse_paged_q4(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                  int32_t num_pages, const int32_t* block_table,
+                                  int32_t max_pages, int32_t page_size, const int32_t* seq_len,
+                                  const int32_t* idx, const int32_t* idx_k, int32_t k_max,
+                                  const int32_t* head_map, float scale, uint16_t* out, float* lse,
+                                  void* stream);
+int kascade_decode_reuse_paged_q4_f16(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                      int32_t num_pages, const int32_t* block_table,
+                                      int32_t max_pages, int32_t page_size, const int32_t* seq_len,
+                                      const int32_t* idx, const int32_t* idx_k, int32_t k_max,
+                                      const int32_t* head_map, float scale, uint16_t* out,
+                                      float* lse, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Calibration (Kascade explainer, レイヤー間類似度とアンカーレイヤー選択 and
  * 動的計画法): which layers are anchors and which anchor KV head each reuse
  * head follows are chosen offline from post-softmax distributions.

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import Shape, check
+from .binding import Q4_ROW_BYTES, Shape, Strides, check
 
 HEAD_DIM = 128
 TILE = 128
@@ -230,6 +230,221 @@ def decode_reuse_paged(q, k_pages, v_pages, block_table, page_size: int, seq_len
         int(k_max), _ptr(head_map), float(scale), _ptr(out), _ptr(lse), _ptr(ws), _ws_bytes(ws),
         _stream())
     check(rc, "kascade_decode_reuse_paged" + sfx)
+    return out, lse
+
+
+# ------------------------------------------------ head norms and rotation ----
+def _need_rows(name: str, t, dtype: torch.dtype, shape: tuple) -> None:
+    """A CUDA tensor of ``shape`` whose last dimension (a row's channels) is
+    contiguous; the other strides are free."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous rows")
+
+
+def _need_one_device(t0: torch.Tensor, **others) -> None:
+    dev = t0.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+
+
+def _call(dev: torch.device, name: str, *args) -> None:
+    """The entry point on the current stream of the tensors' device, which need
+    not be the current device."""
+    fn = getattr(_lib(), name)
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream())
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream())
+    check(rc, name)
+
+
+def _span(t: torch.Tensor):
+    """First byte of a view and the byte after its last."""
+    a = t.data_ptr()
+    return a, a + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _need_apart(name: str, out: torch.Tensor, ins) -> None:
+    """An output is one of its inputs exactly, or shares no memory with any."""
+    if out.numel() == 0:
+        return
+    a, b = _span(out)
+    for t in ins:
+        if t.data_ptr() == a and t.stride() == out.stride() and t.shape == out.shape:
+            return
+    for t in ins:
+        lo, hi = _span(t)
+        if lo < b and a < hi:
+            raise ValueError(f"{name} overlaps an input without being the same view")
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and the rotation by position, in one
+    pass (kascade_qk_norm_rope; the _f16 entry point when q, k are float16).
+
+    q [B, N, Hq, 128] and k [B, N, Hkv, 128] may be views into a packed
+    projection output; positions int32 [B, N]; inv_freq float32 [64];
+    weights [128] of q's type, or None for the rotation alone.  ``interleaved``
+    rotates channels (2i, 2i+1) instead of (i, i + 64).  Returns q [B, Hq, N, 128]
+    and k [B, Hkv, N, 128], the layout of the prefill calls (and, with N = 1,
+    of the decode calls); outputs of that shape with any strides may be given,
+    also the inputs themselves (``q_out=q.transpose(1, 2)``).
+    """
+    B, N, Hq, d = q.shape
+    sfx = _data_suffix(q, k)
+    Hkv = k.shape[2]
+    _need_rows("q", q, q.dtype, (B, N, Hq, d))
+    _need_rows("k", k, q.dtype, (B, N, Hkv, d))
+    _need_size("positions", positions, torch.int32, B * N)
+    _need_size("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need_size(name, w, q.dtype, d)
+    if q_out is None:
+        q_out = torch.empty(B, Hq, N, d, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(B, Hkv, N, d, dtype=q.dtype, device=q.device)
+    _need_rows("q_out", q_out, q.dtype, (B, Hq, N, d))
+    _need_rows("k_out", k_out, q.dtype, (B, Hkv, N, d))
+    _need_one_device(q, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight,
+                     q_out=q_out, k_out=k_out)
+    _need_apart("q_out", q_out, (q.transpose(1, 2), k.transpose(1, 2)))
+    _need_apart("k_out", k_out, (k.transpose(1, 2), q.transpose(1, 2)))
+    _call(q.device, "kascade_qk_norm_rope" + sfx, Shape(B, Hq, Hkv, d), N,
+          _ptr(q), Strides(*q.stride()[:3]), _ptr(k), Strides(*k.stride()[:3]), _ptr(positions), _ptr(inv_freq),
+          _ptr(q_weight), _ptr(k_weight), float(eps), int(bool(interleaved)),
+          _ptr(q_out), Strides(q_out.stride(0), q_out.stride(2), q_out.stride(1)),
+          _ptr(k_out), Strides(k_out.stride(0), k_out.stride(2), k_out.stride(1)))
+    return q_out, k_out
+
+
+# ------------------------------------------------------ 4-bit paged cache ----
+def _need_pages_q4(kv_pages, block_table, B: int, Hkv: int, page_size: int) -> None:
+    """Store [num_pages, Hkv, page_size, 160] and a block table with a row of
+    page numbers for each of the B sequences."""
+    _need_cuda("kv_pages", kv_pages, torch.uint8)
+    _need_cuda("block_table", block_table, torch.int32)
+    if kv_pages.dim() != 4 or tuple(kv_pages.shape[1:]) != (Hkv, page_size, Q4_ROW_BYTES):
+        raise ValueError(
+            f"kv_pages must be [num_pages, {Hkv}, {page_size}, {Q4_ROW_BYTES}], got {tuple(kv_pages.shape)}")
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError(f"block_table must be [>= {B}, max_pages], got {tuple(block_table.shape)}")
+
+
+def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=None):
+    """Quantises K/V rows to 4 bits into the pages (kascade_kv_write_paged_q4; the
+    _f16 entry point when k, v are float16).
+
+    k, v [B, Hkv, N, 128] (any strides, contiguous rows); token n < count[b] of
+    sequence b (all N without ``count``) becomes its token start[b] + n.
+    Returns kv_pages.
+    """
+    B, Hkv, N, d = k.shape
+    sfx = _data_suffix(k, v)
+    _need_rows("k", k, k.dtype, (B, Hkv, N, d))
+    _need_rows("v", v, k.dtype, (B, Hkv, N, d))
+    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
+    _need_size("start", start, torch.int32, B)
+    if count is not None:
+        _need_size("count", count, torch.int32, B)
+    _need_one_device(k, v=v, kv_pages=kv_pages, block_table=block_table, start=start, count=count)
+    _call(k.device, "kascade_kv_write_paged_q4" + sfx, Shape(B, Hkv, Hkv, d), N,
+          _ptr(k), Strides(k.stride(0), k.stride(2), k.stride(1)),
+          _ptr(v), Strides(v.stride(0), v.stride(2), v.stride(1)), _ptr(kv_pages), kv_pages.shape[0],
+          _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count))
+    return kv_pages
+
+
+def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int, dtype=torch.bfloat16,
+                     k=None, v=None):
+    """Reads tokens start[b] .. start[b] + count[b] - 1 of each sequence back in 16
+    bits (kascade_kv_read_paged_q4): k, v [B, Hkv, N, 128]; rows at n >= count[b]
+    are left as they were.  ``count`` None reads N tokens of every sequence."""
+    B = start.numel()
+    Hkv = kv_pages.shape[1]
+    sfx = "_f16" if dtype == torch.float16 else ""
+    if dtype not in _DATA_DTYPES:
+        raise TypeError("dtype must be bfloat16 or float16")
+    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
+    _need_size("start", start, torch.int32, B)
+    if count is not None:
+        _need_size("count", count, torch.int32, B)
+    k = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if k is None else k
+    v = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        _need_size(name, t, dtype, B * Hkv * N * HEAD_DIM)
+    _need_one_device(kv_pages, block_table=block_table, start=start, count=count, k=k, v=v)
+    _call(kv_pages.device, "kascade_kv_read_paged_q4" + sfx, Shape(B, Hkv, Hkv, HEAD_DIM), int(N), _ptr(kv_pages),
+          kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count),
+          _ptr(k), _ptr(v))
+    return k, v
+
+
+def decode_anchor_paged_q4_workspace_bytes(B, Hq, Hkv, max_T) -> int:
+    return int(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(Shape(B, Hq, Hkv, HEAD_DIM), max_T))
+
+
+def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, max_T: int, scale: float, Hkv: int,
+                           out=None, lse=None, pooled=None, ld_pooled: Optional[int] = None, ws=None):
+    """kascade_decode_anchor over a 4-bit paged cache (kascade_decode_anchor_paged_q4;
+    the _f16 entry point when q is float16)."""
+    B, Hq, d = q.shape
+    sfx = _data_suffix(q)
+    _need_cuda("q", q, q.dtype)
+    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
+    _need_size("seq_len", seq_len, torch.int32, B)
+    dev = q.device
+    if ld_pooled is None:
+        ld_pooled = (max_T + 3) // 4 * 4
+    out = torch.empty(B, Hq, d, dtype=q.dtype, device=dev) if out is None else out
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if lse is None else lse
+    pooled = torch.empty(B, Hkv, ld_pooled, dtype=torch.float32, device=dev) if pooled is None else pooled
+    _need_size("out", out, q.dtype, B * Hq * d)
+    _need_size("lse", lse, torch.float32, B * Hq)
+    _need_size("pooled", pooled, torch.float32, B * Hkv * ld_pooled)
+    shape = Shape(B, Hq, Hkv, d)
+    if ws is None:
+        ws = workspace(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T), dev)
+    _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, out=out, lse=lse,
+                     pooled=pooled, ws=ws)
+    _call(dev, "kascade_decode_anchor_paged_q4" + sfx, shape, _ptr(q), _ptr(kv_pages), kv_pages.shape[0],
+          _ptr(block_table), block_table.shape[1], int(page_size), _ptr(seq_len), int(max_T), float(scale),
+          _ptr(out), _ptr(lse), _ptr(pooled), int(ld_pooled), _ptr(ws), _ws_bytes(ws))
+    return out, lse, pooled
+
+
+def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx, idx_k, head_map, scale: float,
+                          Hkv: int, out=None, lse=None):
+    """kascade_decode_reuse over a 4-bit paged cache (kascade_decode_reuse_paged_q4;
+    the _f16 entry point when q is float16)."""
+    B, Hq, d = q.shape
+    sfx = _data_suffix(q)
+    _need_cuda("q", q, q.dtype)
+    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
+    k_max = idx.shape[-1]
+    _need_size("seq_len", seq_len, torch.int32, B)
+    _need_size("idx", idx, torch.int32, B * Hkv * k_max)
+    _need_size("idx_k", idx_k, torch.int32, B * Hkv)
+    _need_size("head_map", head_map, torch.int32, Hkv)
+    dev = q.device
+    out = torch.empty(B, Hq, d, dtype=q.dtype, device=dev) if out is None else out
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if lse is None else lse
+    _need_size("out", out, q.dtype, B * Hq * d)
+    _need_size("lse", lse, torch.float32, B * Hq)
+    _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, idx=idx, idx_k=idx_k,
+                     head_map=head_map, out=out, lse=lse)
+    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, Shape(B, Hq, Hkv, d), _ptr(q), _ptr(kv_pages),
+          kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(seq_len), _ptr(idx),
+          _ptr(idx_k), int(k_max), _ptr(head_map), float(scale), _ptr(out), _ptr(lse))
     return out, lse
 
 

@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(_HERE, "libkascade.so")
 
 KASCADE_OK = 0
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024  # KASCADE_STATIC_SCRATCH_BYTES in include/kascade.h
+Q4_ROW_BYTES = 160  # KASCADE_Q4_ROW_BYTES: one token of one key head, K and V
 STATUS_NAMES = {
     0: "KASCADE_OK",
     1: "KASCADE_ERR_INVALID_ARG",
@@ -48,6 +49,17 @@ EXPORTS = (
     "kascade_decode_reuse_paged",
     "kascade_decode_anchor_paged_f16",
     "kascade_decode_reuse_paged_f16",
+    "kascade_qk_norm_rope",
+    "kascade_qk_norm_rope_f16",
+    "kascade_kv_write_paged_q4",
+    "kascade_kv_write_paged_q4_f16",
+    "kascade_kv_read_paged_q4",
+    "kascade_kv_read_paged_q4_f16",
+    "kascade_decode_anchor_paged_q4_workspace_bytes",
+    "kascade_decode_anchor_paged_q4",
+    "kascade_decode_anchor_paged_q4_f16",
+    "kascade_decode_reuse_paged_q4",
+    "kascade_decode_reuse_paged_q4_f16",
     "kascade_similarity_rows",
     "kascade_similarity_mean_workspace_bytes",
     "kascade_similarity_mean",
@@ -63,6 +75,11 @@ EXPORTS = (
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("d", ctypes.c_int32)]
+
+
+class Strides(ctypes.Structure):
+    """Element strides between sequences, tokens and heads (kascade_strides)."""
+    _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
 
 
 class KascadeError(RuntimeError):
@@ -99,6 +116,16 @@ _SIGNATURES = {
                                                    _F, _P, _P, _P, _I64, _P, _SZ, _P]),
     "kascade_decode_reuse_paged": (ctypes.c_int, [Shape, _P, _P, _P, _I32, _P, _I32, _I32, _P, _P,
                                                   _P, _I32, _P, _F, _P, _P, _P, _SZ, _P]),
+    "kascade_qk_norm_rope": (ctypes.c_int, [Shape, _I32, _P, Strides, _P, Strides, _P, _P, _P, _P, _F, _I32,
+                                            _P, Strides, _P, Strides, _P]),
+    "kascade_kv_write_paged_q4": (ctypes.c_int, [Shape, _I32, _P, Strides, _P, Strides, _P, _I32, _P, _I32, _I32,
+                                                 _P, _P, _P]),
+    "kascade_kv_read_paged_q4": (ctypes.c_int, [Shape, _I32, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P]),
+    "kascade_decode_anchor_paged_q4_workspace_bytes": (_SZ, [Shape, _I32]),
+    "kascade_decode_anchor_paged_q4": (ctypes.c_int, [Shape, _P, _P, _I32, _P, _I32, _I32, _P, _I32, _F, _P, _P,
+                                                      _P, _I64, _P, _SZ, _P]),
+    "kascade_decode_reuse_paged_q4": (ctypes.c_int, [Shape, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _I32, _P,
+                                                     _F, _P, _P, _P]),
     "kascade_similarity_rows": (ctypes.c_int, [_P, _I32, _I64, _P, _P, _P, _P, _I32, _I32, _P, _P,
                                                _P, _P]),
     "kascade_similarity_mean_workspace_bytes": (_SZ, [_I32]),
@@ -114,7 +141,9 @@ _SIGNATURES = {
 }
 # fp16 variants take the same arguments as their bfloat16 counterparts
 for _name in ("kascade_decode_anchor", "kascade_decode_reuse", "kascade_prefill_anchor",
-              "kascade_prefill_reuse", "kascade_decode_anchor_paged", "kascade_decode_reuse_paged"):
+              "kascade_prefill_reuse", "kascade_decode_anchor_paged", "kascade_decode_reuse_paged",
+              "kascade_qk_norm_rope", "kascade_kv_write_paged_q4", "kascade_kv_read_paged_q4",
+              "kascade_decode_anchor_paged_q4", "kascade_decode_reuse_paged_q4"):
     _SIGNATURES[_name + "_f16"] = _SIGNATURES[_name]
 
 _lib = None

@@ -346,6 +346,245 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
                                          stream, true);
 }
 
+// ------------------------------------------- head norms and rotation --
+// Strides of a [B, N, H, 128] view: 16-byte rows, no negative step.
+static bool strides_ok(const kascade_strides& t) {
+  return t.b >= 0 && t.n >= 0 && t.h >= 0 && !((t.b | t.n | t.h) & 7);
+}
+// The same for a view that is written: rows of different (b, n, h) must not be one row.
+static bool out_strides_ok(const kascade_strides& t, int B, int N, int H) {
+  return strides_ok(t) && (B == 1 || t.b >= kHeadDim) && (N == 1 || t.n >= kHeadDim) && (H == 1 || t.h >= kHeadDim);
+}
+
+static int qk_norm_rope_impl(kascade_shape s, int32_t N, const uint16_t* q, kascade_strides q_strides,
+                             const uint16_t* k, kascade_strides k_strides, const int32_t* positions,
+                             const float* inv_freq, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                             int32_t interleaved, uint16_t* q_out, kascade_strides q_out_strides, uint16_t* k_out,
+                             kascade_strides k_out_strides, void* stream, bool f16) {
+  if (s.B < 0 || s.Hq <= 0 || s.Hkv <= 0 || N < 0 || !(eps >= 0.f) || !std::isfinite(eps))
+    return KASCADE_ERR_INVALID_ARG;
+  if (s.d != kHeadDim || (int64_t)s.B * N > kMaxRowLen || s.Hq > 4096 || s.Hkv > 4096)
+    return KASCADE_ERR_UNSUPPORTED_SHAPE;
+  if (s.B == 0 || N == 0) return KASCADE_OK;
+  if (!q || !k || !positions || !inv_freq || !q_out || !k_out || q_out == k_out) return KASCADE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || ((uintptr_t)positions & 3) || ((uintptr_t)inv_freq & 3))
+    return KASCADE_ERR_INVALID_ARG;
+  if (!strides_ok(q_strides) || !strides_ok(k_strides) || !out_strides_ok(q_out_strides, s.B, N, s.Hq) ||
+      !out_strides_ok(k_out_strides, s.B, N, s.Hkv))
+    return KASCADE_ERR_INVALID_ARG;
+  NormRopeParams p = {};
+  p.B = s.B; p.N = N; p.Hq = s.Hq; p.Hkv = s.Hkv;
+  p.q = q; p.k = k; p.q_strides = q_strides; p.k_strides = k_strides;
+  p.positions = positions; p.inv_freq = inv_freq; p.q_weight = q_weight; p.k_weight = k_weight; p.eps = eps;
+  p.interleaved = interleaved != 0; p.f16 = f16;
+  p.q_out = q_out; p.k_out = k_out; p.q_out_strides = q_out_strides; p.k_out_strides = k_out_strides;
+  return from_cuda(launch_qk_norm_rope(p, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_qk_norm_rope(kascade_shape s, int32_t N, const uint16_t* q, kascade_strides q_strides, const uint16_t* k,
+                         kascade_strides k_strides, const int32_t* positions, const float* inv_freq,
+                         const uint16_t* q_weight, const uint16_t* k_weight, float eps, int32_t interleaved,
+                         uint16_t* q_out, kascade_strides q_out_strides, uint16_t* k_out,
+                         kascade_strides k_out_strides, void* stream) {
+  return qk_norm_rope_impl(s, N, q, q_strides, k, k_strides, positions, inv_freq, q_weight, k_weight, eps, interleaved,
+                           q_out, q_out_strides, k_out, k_out_strides, stream, false);
+}
+
+int kascade_qk_norm_rope_f16(kascade_shape s, int32_t N, const uint16_t* q, kascade_strides q_strides,
+                             const uint16_t* k, kascade_strides k_strides, const int32_t* positions,
+                             const float* inv_freq, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                             int32_t interleaved, uint16_t* q_out, kascade_strides q_out_strides, uint16_t* k_out,
+                             kascade_strides k_out_strides, void* stream) {
+  return qk_norm_rope_impl(s, N, q, q_strides, k, k_strides, positions, inv_freq, q_weight, k_weight, eps, interleaved,
+                           q_out, q_out_strides, k_out, k_out_strides, stream, true);
+}
+
+// ------------------------------------------------------ 4-bit paged cache --
+static int check_pages_q4(const uint8_t* kv_pages, const int32_t* block_table, int32_t num_pages, int32_t max_pages,
+                          int32_t page_size) {
+  if (!kv_pages || !block_table || num_pages < 1 || max_pages < 1 || page_size < 16 || (page_size % 16))
+    return KASCADE_ERR_INVALID_ARG;
+  if (!aligned16(kv_pages) || ((uintptr_t)block_table & 3)) return KASCADE_ERR_INVALID_ARG;
+  return KASCADE_OK;
+}
+
+// Shape checks of the cache's write and read back (Hq is not used).
+static int check_cache_shape(const kascade_shape& s, int32_t N) {
+  if (s.B < 0 || s.Hkv <= 0 || N < 0) return KASCADE_ERR_INVALID_ARG;
+  if (s.d != kHeadDim || (int64_t)s.B * N > kMaxRowLen || s.Hkv > 4096) return KASCADE_ERR_UNSUPPORTED_SHAPE;
+  return KASCADE_OK;
+}
+
+static int kv_write_paged_q4_impl(kascade_shape s, int32_t N, const uint16_t* k, kascade_strides k_strides,
+                                  const uint16_t* v, kascade_strides v_strides, uint8_t* kv_pages, int32_t num_pages,
+                                  const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                  const int32_t* start, const int32_t* count, void* stream, bool f16) {
+  int rc = check_cache_shape(s, N);
+  if (rc || s.B == 0 || N == 0) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if (!k || !v || !start || !aligned16(k) || !aligned16(v) || ((uintptr_t)start & 3) || ((uintptr_t)count & 3) ||
+      !strides_ok(k_strides) || !strides_ok(v_strides))
+    return KASCADE_ERR_INVALID_ARG;
+  CacheQ4Params p = {};
+  p.B = s.B; p.N = N; p.Hkv = s.Hkv; p.f16 = f16;
+  p.k = k; p.v = v; p.k_strides = k_strides; p.v_strides = v_strides;
+  p.kv_pages = kv_pages; p.block_table = block_table;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size;
+  p.start = start; p.count = count;
+  p.status = device_status_ptr();
+  if (!p.status) return KASCADE_ERR_CUDA;
+  return from_cuda(launch_cache_q4(p, true, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_kv_write_paged_q4(kascade_shape s, int32_t N, const uint16_t* k, kascade_strides k_strides,
+                              const uint16_t* v, kascade_strides v_strides, uint8_t* kv_pages, int32_t num_pages,
+                              const int32_t* block_table, int32_t max_pages, int32_t page_size, const int32_t* start,
+                              const int32_t* count, void* stream) {
+  return kv_write_paged_q4_impl(s, N, k, k_strides, v, v_strides, kv_pages, num_pages, block_table, max_pages,
+                                page_size, start, count, stream, false);
+}
+
+int kascade_kv_write_paged_q4_f16(kascade_shape s, int32_t N, const uint16_t* k, kascade_strides k_strides,
+                                  const uint16_t* v, kascade_strides v_strides, uint8_t* kv_pages, int32_t num_pages,
+                                  const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                  const int32_t* start, const int32_t* count, void* stream) {
+  return kv_write_paged_q4_impl(s, N, k, k_strides, v, v_strides, kv_pages, num_pages, block_table, max_pages,
+                                page_size, start, count, stream, true);
+}
+
+static int kv_read_paged_q4_impl(kascade_shape s, int32_t N, const uint8_t* kv_pages, int32_t num_pages,
+                                 const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                 const int32_t* start, const int32_t* count, uint16_t* k, uint16_t* v, void* stream,
+                                 bool f16) {
+  int rc = check_cache_shape(s, N);
+  if (rc || s.B == 0 || N == 0) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if (!k || !v || k == v || !start || !aligned16(k) || !aligned16(v) || ((uintptr_t)start & 3) ||
+      ((uintptr_t)count & 3))
+    return KASCADE_ERR_INVALID_ARG;
+  CacheQ4Params p = {};
+  p.B = s.B; p.N = N; p.Hkv = s.Hkv; p.f16 = f16;
+  p.k_out = k; p.v_out = v;
+  p.kv_pages = const_cast<uint8_t*>(kv_pages); p.block_table = block_table;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size;
+  p.start = start; p.count = count;
+  p.status = device_status_ptr();
+  if (!p.status) return KASCADE_ERR_CUDA;
+  return from_cuda(launch_cache_q4(p, false, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_kv_read_paged_q4(kascade_shape s, int32_t N, const uint8_t* kv_pages, int32_t num_pages,
+                             const int32_t* block_table, int32_t max_pages, int32_t page_size, const int32_t* start,
+                             const int32_t* count, uint16_t* k, uint16_t* v, void* stream) {
+  return kv_read_paged_q4_impl(s, N, kv_pages, num_pages, block_table, max_pages, page_size, start, count, k, v,
+                               stream, false);
+}
+
+int kascade_kv_read_paged_q4_f16(kascade_shape s, int32_t N, const uint8_t* kv_pages, int32_t num_pages,
+                                 const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                 const int32_t* start, const int32_t* count, uint16_t* k, uint16_t* v, void* stream) {
+  return kv_read_paged_q4_impl(s, N, kv_pages, num_pages, block_table, max_pages, page_size, start, count, k, v,
+                               stream, true);
+}
+
+size_t kascade_decode_anchor_paged_q4_workspace_bytes(kascade_shape s, int32_t max_T) {
+  if (check_shape(s) != KASCADE_OK || max_T < 0 || max_T > kMaxRowLen || decode_logits_too_large(s, max_T)) return 0;
+  return decode_q4_workspace_bytes(s.B, s.Hkv, s.Hq / s.Hkv, max_T);
+}
+
+static int decode_anchor_paged_q4_impl(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                       const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                       const int32_t* seq_len, int32_t max_T, float scale, uint16_t* out, float* lse,
+                                       float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream,
+                                       bool f16) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if (max_T < 0 || ld_pooled < max_T || (ld_pooled & 3) || !std::isfinite(scale)) return KASCADE_ERR_INVALID_ARG;
+  if (max_T > kMaxRowLen || decode_logits_too_large(s, max_T) || s.B > 65535 || s.Hkv > 65535)
+    return KASCADE_ERR_UNSUPPORTED_SHAPE;
+  if (s.B == 0) return KASCADE_OK;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if ((int64_t)max_pages * page_size < max_T) return KASCADE_ERR_INVALID_ARG;
+  if (!q || !seq_len || !out || (max_T > 0 && !pooled) || !ws) return KASCADE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(pooled) || !aligned16(ws) || !aligned16(lse) ||
+      ((uintptr_t)seq_len & 3))
+    return KASCADE_ERR_INVALID_ARG;
+  if (ws_bytes < kascade_decode_anchor_paged_q4_workspace_bytes(s, max_T)) return KASCADE_ERR_WORKSPACE_TOO_SMALL;
+  DecodeQ4Params p = {};
+  p.B = s.B; p.Hq = s.Hq; p.Hkv = s.Hkv; p.G = s.Hq / s.Hkv; p.f16 = f16;
+  p.q = q; p.kv_pages = kv_pages; p.block_table = block_table;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size;
+  p.seq_len = seq_len; p.max_T = max_T;
+  p.scale = scale; p.out = out; p.lse = lse; p.pooled = pooled; p.ld_pooled = ld_pooled;
+  p.ws = ws;
+  p.status = device_status_ptr();
+  if (!p.status) return KASCADE_ERR_CUDA;
+  return from_cuda(launch_decode_anchor_q4(p, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_decode_anchor_paged_q4(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                   const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                   const int32_t* seq_len, int32_t max_T, float scale, uint16_t* out, float* lse,
+                                   float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream) {
+  return decode_anchor_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, max_T,
+                                     scale, out, lse, pooled, ld_pooled, ws, ws_bytes, stream, false);
+}
+
+int kascade_decode_anchor_paged_q4_f16(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                       const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                       const int32_t* seq_len, int32_t max_T, float scale, uint16_t* out, float* lse,
+                                       float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream) {
+  return decode_anchor_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, max_T,
+                                     scale, out, lse, pooled, ld_pooled, ws, ws_bytes, stream, true);
+}
+
+static int decode_reuse_paged_q4_impl(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                      const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                      const int32_t* seq_len, const int32_t* idx, const int32_t* idx_k, int32_t k_max,
+                                      const int32_t* head_map, float scale, uint16_t* out, float* lse, void* stream,
+                                      bool f16) {
+  int rc = check_shape(s);
+  if (rc) return rc;
+  if (k_max < 0 || !std::isfinite(scale)) return KASCADE_ERR_INVALID_ARG;
+  if (k_max > kMaxRowLen || s.B > 65535 || s.Hkv > 65535) return KASCADE_ERR_UNSUPPORTED_SHAPE;
+  if (s.B == 0) return KASCADE_OK;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if (!q || !seq_len || (k_max > 0 && !idx) || !idx_k || !head_map || !out) return KASCADE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ((uintptr_t)seq_len & 3) || ((uintptr_t)idx & 3) ||
+      ((uintptr_t)idx_k & 3) || ((uintptr_t)head_map & 3))
+    return KASCADE_ERR_INVALID_ARG;
+  DecodeQ4Params p = {};
+  p.B = s.B; p.Hq = s.Hq; p.Hkv = s.Hkv; p.G = s.Hq / s.Hkv; p.f16 = f16;
+  p.q = q; p.kv_pages = kv_pages; p.block_table = block_table;
+  p.num_pages = num_pages; p.max_pages = max_pages; p.page_size = page_size;
+  p.seq_len = seq_len;
+  // a sequence longer than its block table's pages is flagged and skipped
+  const int64_t cap = (int64_t)max_pages * page_size;
+  p.max_T = cap > kMaxRowLen ? kMaxRowLen : (int)cap;
+  p.idx = idx; p.idx_k = idx_k; p.head_map = head_map; p.k_max = k_max;
+  p.scale = scale; p.out = out; p.lse = lse;
+  p.status = device_status_ptr();
+  if (!p.status) return KASCADE_ERR_CUDA;
+  return from_cuda(launch_decode_reuse_q4(p, static_cast<cudaStream_t>(stream)));
+}
+
+int kascade_decode_reuse_paged_q4(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                  const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                  const int32_t* seq_len, const int32_t* idx, const int32_t* idx_k, int32_t k_max,
+                                  const int32_t* head_map, float scale, uint16_t* out, float* lse, void* stream) {
+  return decode_reuse_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, idx, idx_k,
+                                    k_max, head_map, scale, out, lse, stream, false);
+}
+
+int kascade_decode_reuse_paged_q4_f16(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,
+                                      const int32_t* block_table, int32_t max_pages, int32_t page_size,
+                                      const int32_t* seq_len, const int32_t* idx, const int32_t* idx_k, int32_t k_max,
+                                      const int32_t* head_map, float scale, uint16_t* out, float* lse, void* stream) {
+  return decode_reuse_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, idx, idx_k,
+                                    k_max, head_map, scale, out, lse, stream, true);
+}
+
 // -------------------------------------------------------------------- topk --
 size_t kascade_topk_workspace_bytes(int32_t rows, int64_t ld) {
   (void)rows;

@@ -53,6 +53,67 @@ int decode_anchor_check_args(kascade_shape s, const uint16_t* q, const uint16_t*
                              const uint16_t* out, const float* lse, const float* pooled, int64_t ld_pooled);
 cudaError_t launch_decode_reuse(const DecodeParams& p, cudaStream_t st);
 
+// ----------------------------------------- head norms and rotation ----
+struct NormRopeParams {
+  int B, N, Hq, Hkv;
+  const uint16_t* q;
+  const uint16_t* k;
+  kascade_strides q_strides, k_strides;
+  const int32_t* positions;
+  const float* inv_freq;
+  const uint16_t* q_weight;  // NULL: no norm
+  const uint16_t* k_weight;
+  float eps;
+  bool interleaved, f16;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  kascade_strides q_out_strides, k_out_strides;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t st);
+
+// ------------------------------------------------------ 4-bit paged cache ----
+struct CacheQ4Params {
+  int B, N, Hkv;
+  bool f16;
+  const uint16_t* k;  // write
+  const uint16_t* v;
+  kascade_strides k_strides, v_strides;
+  uint16_t* k_out;    // read back
+  uint16_t* v_out;
+  uint8_t* kv_pages;
+  const int32_t* block_table;
+  int num_pages, max_pages, page_size;
+  const int32_t* start;
+  const int32_t* count;
+  unsigned* status;
+};
+cudaError_t launch_cache_q4(const CacheQ4Params& p, bool write, cudaStream_t st);
+
+struct DecodeQ4Params {
+  int B, Hq, Hkv, G;
+  bool f16;
+  const uint16_t* q;
+  const uint8_t* kv_pages;
+  const int32_t* block_table;
+  int num_pages, max_pages, page_size;
+  const int32_t* seq_len;
+  int max_T;
+  const int32_t* idx;  // reuse
+  const int32_t* idx_k;
+  const int32_t* head_map;
+  int k_max;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  float* pooled;  // anchor
+  int64_t ld_pooled;
+  void* ws;
+  unsigned* status;
+};
+size_t decode_q4_workspace_bytes(int B, int Hkv, int G, int max_T);
+cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st);
+cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st);
+
 // ------------------------------------------------------------------ topk ----
 size_t topk_smem_bytes(int64_t ld);
 cudaError_t launch_topk(const float* scores, int rows, int64_t ld, const int32_t* row_len,

@@ -1,0 +1,153 @@
+// RMS norm of query and key heads and the rotation by position, in one pass.
+//
+// For a head row x of 128 channels, weight w and position p:
+//   y = x * rsqrt(mean(x^2) + eps) * w        (y = x without a weight)
+//   pair i of 64: angle a = p * inv_freq[i];  (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a)
+// with j = i + 64 (half split), or channels (2i, 2i+1) (interleaved).  All of it
+// is fp32 in registers, rounded once when the row is stored.
+//
+// The angle.  p * inv_freq in fp32 is off by p * 2^-24 radians (0.008 at a
+// position of 131072), so it is formed in 64 bits as turns, reduced to
+// [-1/2, 1/2] there, and only then handed to sincospif in fp32.  It is the same
+// for every head of a token: a block computes its tokens' 64 pairs once, into
+// shared memory, and all its heads read them.
+//
+// What bounds it: memory (a row is read and written once, 4 bytes per channel
+// in all).  A row is 8 lanes x two 16-byte chunks, channels 8j.. and 64 + 8j..,
+// so both halves of a half-split pair are in one lane and nothing is exchanged
+// but the sum of squares.
+#include "common.cuh"
+#include "internal.h"
+#include "q4.cuh"
+
+namespace kascade {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = kThreads / 8;  // rows a block works on at a time
+
+struct RopeArgs {
+  const uint16_t* x[2];  // q, k
+  uint16_t* y[2];
+  const uint16_t* w[2];  // weights, or NULL
+  kascade_strides xs[2], ys[2];
+  const int32_t* pos;
+  const float* inv_freq;
+  float eps;
+  int N, Hq, H;          // tokens per sequence; query heads; all heads
+  int tiles;             // token tiles per sequence
+  int heads_per_block;
+};
+
+// TOK tokens x kRows / TOK heads at a time.
+template <int TOK, bool F16, bool INTER>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
+  __shared__ float2 cs[TOK][kHeadDim / 2];
+  const int b = blockIdx.x / a.tiles;
+  const int n0 = (blockIdx.x - b * a.tiles) * TOK;
+  for (int e = threadIdx.x; e < TOK * (kHeadDim / 2); e += kThreads) {
+    const int t = e / (kHeadDim / 2), i = e % (kHeadDim / 2);
+    const int n = min(n0 + t, a.N - 1);
+    constexpr double kInvTwoPi = 0.15915494309189533577;
+    const double turns = (double)a.pos[(int64_t)b * a.N + n] * (double)a.inv_freq[i] * kInvTwoPi;
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    cs[t][i] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  const int row = threadIdx.x / 8, j = threadIdx.x % 8;
+  const int t = row % TOK, n = n0 + t;
+  const int h_end = min(a.H, (int)(blockIdx.y + 1) * a.heads_per_block);
+  for (int hh = blockIdx.y * a.heads_per_block; hh < h_end; hh += kRows / TOK) {
+    // a warp's four rows may lie past the end: they compute on the last row and store nothing
+    const int h = min(hh + row / TOK, h_end - 1);
+    const bool live = hh + row / TOK < h_end && n < a.N;
+    const int part = h >= a.Hq;
+    const int hp = part ? h - a.Hq : h;
+    const kascade_strides& xs = a.xs[part];
+    const uint16_t* x = a.x[part] + (int64_t)b * xs.b + (int64_t)min(n, a.N - 1) * xs.n + (int64_t)hp * xs.h + 8 * j;
+    const uint4 c0 = ldg16(x), c1 = ldg16(x + 64);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack2<F16>(word_of(c0, i), v[2 * i], v[2 * i + 1]);
+      unpack2<F16>(word_of(c1, i), v[8 + 2 * i], v[8 + 2 * i + 1]);
+    }
+    if (a.w[part]) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss += v[i] * v[i];
+      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+      const float r = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
+      const uint4 w0 = ldg16(a.w[part] + 8 * j), w1 = ldg16(a.w[part] + 64 + 8 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2<F16>(word_of(w0, i), lo, hi);
+        v[2 * i] *= r * lo;
+        v[2 * i + 1] *= r * hi;
+        unpack2<F16>(word_of(w1, i), lo, hi);
+        v[8 + 2 * i] *= r * lo;
+        v[8 + 2 * i + 1] *= r * hi;
+      }
+    }
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (INTER) {  // pairs (2i, 2i+1) of chunk 0, then of chunk 1
+        const float2 r = cs[t][i < 4 ? 4 * j + i : 32 + 4 * j + i - 4];
+        o[2 * i] = v[2 * i] * r.x - v[2 * i + 1] * r.y;
+        o[2 * i + 1] = v[2 * i + 1] * r.x + v[2 * i] * r.y;
+      } else {                // channel 8j + i with 64 + 8j + i
+        const float2 r = cs[t][8 * j + i];
+        o[i] = v[i] * r.x - v[8 + i] * r.y;
+        o[8 + i] = v[8 + i] * r.x + v[i] * r.y;
+      }
+    }
+    if (live) {
+      const kascade_strides& ys = a.ys[part];
+      uint16_t* y = a.y[part] + (int64_t)b * ys.b + (int64_t)n * ys.n + (int64_t)hp * ys.h + 8 * j;
+      *reinterpret_cast<uint4*>(y) = make_uint4(pack_x2<F16>(o[0], o[1]), pack_x2<F16>(o[2], o[3]),
+                                                pack_x2<F16>(o[4], o[5]), pack_x2<F16>(o[6], o[7]));
+      *reinterpret_cast<uint4*>(y + 64) = make_uint4(pack_x2<F16>(o[8], o[9]), pack_x2<F16>(o[10], o[11]),
+                                                     pack_x2<F16>(o[12], o[13]), pack_x2<F16>(o[14], o[15]));
+    }
+  }
+}
+
+template <int TOK>
+cudaError_t launch_tok(RopeArgs& a, int B, bool f16, bool interleaved, cudaStream_t st) {
+  a.tiles = (a.N + TOK - 1) / TOK;
+  const int64_t blocks = (int64_t)B * a.tiles;
+  // Few tokens: the heads go to several blocks, until there are about four blocks per SM.
+  constexpr int kStep = kRows / TOK;
+  const int steps = (a.H + kStep - 1) / kStep;
+  int split = (int)((4 * 148 + blocks - 1) / blocks);
+  if (split > steps) split = steps;
+  a.heads_per_block = (steps + split - 1) / split * kStep;
+  const dim3 grid((unsigned)blocks, (a.H + a.heads_per_block - 1) / a.heads_per_block);
+  auto kern = f16 ? (interleaved ? qk_norm_rope_kernel<TOK, true, true> : qk_norm_rope_kernel<TOK, true, false>)
+                  : (interleaved ? qk_norm_rope_kernel<TOK, false, true> : qk_norm_rope_kernel<TOK, false, false>);
+  kern<<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const NormRopeParams& p, cudaStream_t st) {
+  RopeArgs a;
+  a.x[0] = p.q; a.x[1] = p.k; a.y[0] = p.q_out; a.y[1] = p.k_out;
+  a.w[0] = p.q_weight; a.w[1] = p.k_weight;
+  a.xs[0] = p.q_strides; a.xs[1] = p.k_strides; a.ys[0] = p.q_out_strides; a.ys[1] = p.k_out_strides;
+  a.pos = p.positions; a.inv_freq = p.inv_freq; a.eps = p.eps;
+  a.N = p.N; a.Hq = p.Hq; a.H = p.Hq + p.Hkv;
+  // Four tokens per block share their pairs' cosines with four heads at a time; with fewer tokens
+  // per sequence that many lanes would idle, so each block takes one token and 16 heads at a time.
+  return p.N >= 4 ? launch_tok<4>(a, p.B, p.f16, p.interleaved, st) : launch_tok<1>(a, p.B, p.f16, p.interleaved, st);
+}
+
+}  // namespace kascade

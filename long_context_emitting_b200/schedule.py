@@ -86,6 +86,64 @@ class DecodeSchedule:
                 self.run_reuse(layers[l], head_maps[l], outs[l])
 
 
+class PagedQ4DecodeSchedule(DecodeSchedule):
+    """One decode step over 4-bit paged caches, from the projections' outputs.
+
+    Every layer normalises and rotates the new token's queries and keys, appends
+    its K/V to the layer's pages in 4 bits and then attends (anchor layers to
+    everything, reuse layers to the latest anchor's indices).  ``lens`` counts
+    the new token, so it goes to position lens[b] - 1; a sequence of length 0 is
+    a padded row of the batch: nothing is appended and its output is 0.
+
+    A layer's inputs are a dict of q [B, 1, Hq, 128], k and v [B, 1, Hkv, 128]
+    (views into one projection output will do), kv_pages and block_table
+    (paging.q4_store), and optionally q_weight and k_weight [128].
+    """
+
+    def __init__(self, B: int, Hq: int, Hkv: int, lens: Sequence[int], anchors: Sequence[int],
+                 n_layers: int, device, inv_freq: torch.Tensor, dtype=torch.bfloat16, eps: float = 1e-6,
+                 interleaved: bool = False, scale: Optional[float] = None):
+        super().__init__(B, Hq, Hkv, lens, anchors, n_layers, device, scale)
+        self.inv_freq, self.eps, self.interleaved = inv_freq, eps, interleaved
+        last = [max(T - 1, 0) for T in self.lens]
+        self.seq_len = torch.tensor(self.lens, dtype=torch.int32, device=device)
+        self.positions = torch.tensor(last, dtype=torch.int32, device=device)
+        self.count = torch.tensor([min(T, 1) for T in self.lens], dtype=torch.int32, device=device)
+        self.q = torch.empty(B, Hq, 1, self.d, dtype=dtype, device=device)
+        self.k = torch.empty(B, Hkv, 1, self.d, dtype=dtype, device=device)
+        self.ws = api.workspace(api.decode_anchor_paged_q4_workspace_bytes(B, Hq, Hkv, self.max_T), device)
+
+    def run_append(self, layer_in: Dict):
+        api.qk_norm_rope(layer_in["q"], layer_in["k"], self.positions, self.inv_freq,
+                         q_weight=layer_in.get("q_weight"), k_weight=layer_in.get("k_weight"), eps=self.eps,
+                         interleaved=self.interleaved, q_out=self.q, k_out=self.k)
+        pages = layer_in["kv_pages"]
+        api.kv_write_paged_q4(self.k, layer_in["v"].transpose(1, 2), pages, layer_in["block_table"],
+                              pages.shape[2], self.positions, self.count)
+
+    def run_anchor(self, layer_in: Dict, out: torch.Tensor):
+        pages = layer_in["kv_pages"]
+        api.decode_anchor_paged_q4(self.q.squeeze(2), pages, layer_in["block_table"], pages.shape[2],
+                                   self.seq_len, self.max_T, self.scale, self.Hkv, out=out, lse=self.lse,
+                                   pooled=self.pooled, ld_pooled=self.ld, ws=self.ws)
+
+    def run_reuse(self, layer_in: Dict, head_map: torch.Tensor, out: torch.Tensor):
+        pages = layer_in["kv_pages"]
+        api.decode_reuse_paged_q4(self.q.squeeze(2), pages, layer_in["block_table"], pages.shape[2],
+                                  self.seq_len, self.idx, self.row_k, head_map, self.scale, self.Hkv, out=out,
+                                  lse=self.lse)
+
+    def step(self, layers: List[Dict], head_maps: Dict[int, torch.Tensor],
+             outs: List[torch.Tensor]):
+        for l in range(self.n_layers):
+            self.run_append(layers[l])
+            if self.is_anchor(l):
+                self.run_anchor(layers[l], outs[l])
+                self.run_topk()
+            else:
+                self.run_reuse(layers[l], head_maps[l], outs[l])
+
+
 class PrefillSchedule:
     """Prefill of N tokens (batch B) through ``n_layers`` layers."""
 

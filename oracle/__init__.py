@@ -5,3 +5,4 @@ Only tests, ``__graft_entry__.smoke()`` and the CPU-baseline legs of
 """
 from .kascade_oracle import *  # noqa: F401,F403
 from .kascade_oracle import __all__  # noqa: F401
+from .cache_oracle import *  # noqa: F401,F403

@@ -1,16 +1,49 @@
 // Decode attention over the 4-bit paged cache (row format in q4.cuh): the anchor
 // (every token, pooled probabilities) and the reuse layer (selected tokens).
 //
-// With V, K = minimum + scale * code per row and group, for each query head:
+// With K, V = minimum + scale * code per row and group, for each query head:
 //   s_t = scale · q · K_t;  out = sum_t softmax(s)_t V_t;  lse = log sum_t exp(s_t)
 //
-// A warp takes one token at a time: lane l holds channels 4l .. 4l + 3, so its
-// four K codes are one half word, its four V codes another, and both belong to
-// scale group l / 8.  All arithmetic is fp32.  The anchor's splits go through
-// the workspace and a combine kernel; a reuse row is one block.
+// The codes are never turned into values.  A group's scale and minimum are the
+// same for its 32 channels, so
+//   q · K_t    = sum_g [ ks_{t,g} (q_g · n_{t,g}) + km_{t,g} sum(q_g) ]
+//   out_d      = sum_t (p_t vs_{t,g}) n_{t,d}  +  sum_t p_t vm_{t,g}      (d in group g)
+// and mma.sync multiplies the codes n themselves: a nibble masked into the low
+// or the next four bits of a half word is the half-precision subnormal n · 2^-24
+// or n · 2^-20, exact, so eight codes cost one shift and four ANDs.  The other
+// operand carries the powers of two: q (scaled per head so that its largest
+// element is near 2^14; a bfloat16 or half q is then exact in half precision
+// down to 2^-29 of that) and p · vs (below).
+//   * S^T[16 tokens x 8 heads]: two m16n8k16 per scale group, whose fp32 sums
+//     the row's scales weight; the minima come in by one more mma, bfloat16
+//     minima against sum(q_g) split into three bfloat16 terms (24 bits).
+//   * O^T[128 channels x 8 heads]: per group the weights p · vs, rounded to half
+//     precision (at most 2^-11 of each weight, independently: as fine as a half
+//     output's rounding before it averages over the tokens), are the B operand.
+//     Weights of different tokens may differ by any power of two, so each head
+//     and group has its own factor c, a power of two: the first weights, and any
+//     that would pass 2^15, are put near 2^8, where weights 2^22 times smaller
+//     still keep all their bits.  When the running maximum moves, c takes up the
+//     change and the sums stay.  The minima are summed in fp32 (8 sums per lane).
+//   * The running maximum moves only when a score exceeds it by 8 (weights then
+//     reach 2^8 instead of 1), so most blocks need one vote instead of a
+//     reduction and a rescale of the sums.
+//
+// What bounds it: the cache's bytes (160 per token and key head) and, close
+// behind, instruction issue: about 270 warp instructions per 16 tokens.  A warp
+// owns a run of tokens and a ring of 32-row stages in shared memory that bulk
+// copies fill: 16 tokens from a page boundary are 2560 adjacent bytes, so the
+// anchor's stage is two copies; a reuse stage is 32 copies of one row.  No
+// registers hold data in flight.  Rows lie 160 bytes apart, which is 8 banks
+// mod 32; the fragment rows are taken in the order 0 6 1 7 2 4 3 5 so that the
+// 16-byte K reads (pairs of rows) and the 8-byte V reads (every second fragment
+// row) both meet different banks.
 #include "common.cuh"
 #include "internal.h"
 #include "q4.cuh"
+#include "tcgen05.cuh"
+
+#include <cooperative_groups.h>
 
 #include <cmath>
 
@@ -20,7 +53,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kStageRows = 32;
+constexpr int kStages = 2;
+constexpr uint32_t kStageBytes = kStageRows * kQ4Row;
+constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+constexpr uint32_t kSmemBytes = kRingBytes + 128;
 constexpr float kLn2 = 0.6931471805599453f;
+static_assert(kRingBytes >= kWarps * 8 * kHeadDim * sizeof(float), "the merge overlays the rings");
 
 struct Q4Args {
   const uint16_t* q;
@@ -32,8 +71,8 @@ struct Q4Args {
   const int32_t* idx_k;
   const int32_t* head_map;
   int k_max;
-  int Hq, Hkv, max_T;
-  int tok_per_warp, nsplit;
+  int Hq, Hkv, G, max_T;
+  int tok_per_warp, nsplit;  // tok_per_warp is a multiple of 16
   float scale_log2;
   float* logits;   // anchor: [B, Hkv, max_T, G] base-2 scaled logits
   float* part_ml;  // [B*Hkv, nsplit, G, 2]
@@ -49,106 +88,431 @@ struct Q4Args {
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ float lse2_of(float m, float l) { return l == 0.f ? -INFINITY : finite_max(m) + __log2f(l); }
 
-template <int G, bool GATHER, bool F16>
-__global__ void __launch_bounds__(kThreads) decode_q4_kernel(const Q4Args a) {
-  __shared__ float sm_o[kWarps][G][kHeadDim];
-  __shared__ float sm_m[kWarps][G], sm_l[kWarps][G];
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
+  return r;
+}
+
+// Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) that completes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// 2^e as a float, -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The query operand: heads are the 8 columns, head gid of a lane's fragments.
+struct Query {
+  uint32_t b[4][4];   // per scale group: the two k16 steps' b0, b1
+  uint32_t s0, s1;    // sum(q_g) against the minima
+  float f0, f1;       // factors of heads 2 tig, 2 tig + 1 to base-2 logits
+};
+
+template <bool F16>
+__device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, float scale_log2, int gid, int tig) {
+  float v[4][8];
+  float top = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    // columns gid >= G are padding: load a valid row and zero it
+    uint4 w = ldg16(q + (gid < G ? gid : G - 1) * kHeadDim + 32 * g + 8 * tig);
+    if (gid >= G) w = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack2<F16>(word_of(w, i), v[g][2 * i], v[g][2 * i + 1]);
+      top = fmaxf(top, fmaxf(fabsf(v[g][2 * i]), fabsf(v[g][2 * i + 1])));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // q' = q 2^-e with its largest element in [2^14, 2^15); e = 0 for a zero or non-finite head
+  int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;
+  if (!(top > 0.f) || e > 127 - 14) e = 0;
+  e = max(e, -120);
+  const float down = pow2i(-e);
+  float sum[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    sum[g] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[g][i] *= down;
+      sum[g] += v[g][i];
+    }
+    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+    sum[g] *= 0x1p-24f;  // the codes' unit
+    // code j of a word is in half j / 4; odd j carry 16 times their code
+    x.b[g][0] = pack_f16x2(v[g][0], v[g][4]);
+    x.b[g][1] = pack_f16x2(v[g][1] * 0.0625f, v[g][5] * 0.0625f);
+    x.b[g][2] = pack_f16x2(v[g][2], v[g][6]);
+    x.b[g][3] = pack_f16x2(v[g][3] * 0.0625f, v[g][7] * 0.0625f);
+  }
+  // k = 0..3: leading term of sum_g against minimum g, 4..7: second, 8..11: third, 12..15: nothing
+  const float u0 = (tig & 1) ? sum[2] : sum[0], u1 = (tig & 1) ? sum[3] : sum[1];
+  const uint32_t hi = pack_bf16x2(u0, u1);
+  const float r0 = u0 - bf16_lo(hi), r1 = u1 - bf16_hi(hi);
+  const uint32_t mid = pack_bf16x2(r0, r1);
+  const uint32_t lo = pack_bf16x2(r0 - bf16_lo(mid), r1 - bf16_hi(mid));
+  x.s0 = tig < 2 ? hi : mid;
+  x.s1 = tig < 2 ? lo : 0u;
+  const float f = scale_log2 * pow2i(e);
+  x.f0 = __shfl_sync(0xffffffffu, f, 8 * tig);
+  x.f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+}
+
+// Base-2 logits of 16 rows at shared address `rows`: s[0], s[1] are heads 2 tig, 2 tig + 1 of the
+// lane's row a, s[2], s[3] of row b = a + 8.
+__device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t row_a, int tig, float (&s)[4]) {
+  const uint32_t a = rows + row_a, b = a + 8 * kQ4Row;
+  const uint4 ka = lds128(a + 16 * tig), kb = lds128(b + 16 * tig);
+  const uint4 ta = lds128(a + kQ4Tail), tb = lds128(b + kQ4Tail);
+  float c[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t ma = (tig & 1) ? ta.w : ta.z, mb = (tig & 1) ? tb.w : tb.z;
+  mma_bf16_16816(c, ma, mb, ma, mb, x.s0, x.s1);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t wa = word_of(ka, g), wb = word_of(kb, g);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_f16_16816(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, x.b[g][0], x.b[g][1]);
+    const uint32_t ha = wa >> 8, hb = wb >> 8;
+    mma_f16_16816(d, ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u, x.b[g][2], x.b[g][3]);
+    const uint32_t sa = g < 2 ? ta.x : ta.y, sb = g < 2 ? tb.x : tb.y;
+    const float fa = (g & 1) ? bf16_hi(sa) : bf16_lo(sa), fb = (g & 1) ? bf16_hi(sb) : bf16_lo(sb);
+    c[0] = fmaf(fa, d[0], c[0]);
+    c[1] = fmaf(fa, d[1], c[1]);
+    c[2] = fmaf(fb, d[2], c[2]);
+    c[3] = fmaf(fb, d[3], c[3]);
+  }
+  s[0] = c[0] * 0x1p24f * x.f0;
+  s[1] = c[1] * 0x1p24f * x.f1;
+  s[2] = c[2] * 0x1p24f * x.f0;
+  s[3] = c[3] * 0x1p24f * x.f1;
+}
+
+// Running state of a warp: heads 2 tig, 2 tig + 1.
+struct State {
+  float m0, m1, l0, l1;
+  float o[4][2][4];  // [group][channel pair]: rows gid = channel 4 gid + 2 pair, gid + 8 = the next (times 16)
+  float z[4][2];     // sums of p · vm, this lane's rows
+  float c[4][2];     // [group][head]: the sums o and the weights that enter them are times this power of two
+};
+
+constexpr float kMaxC = 0x1p100f;
+
+// A weight has reached 2^15: new factors, which put the largest weight of each head and group that
+// did so in [2^7, 2^8).  x: p · vs / c of the lane's rows (not finite: it spoils its own sum only).
+__device__ __noinline__ float lower_c(float c, float x) {
+  x = x < INFINITY ? x : 0.f;
+  x = warp_max_xor_gid(x);
+  const int e = max((int)(__float_as_uint(x) >> 23), 27);  // biased; c stays within 2^107
+  return x * c < 0x1p15f ? c : __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23);
+}
+
+// The weights' unit grows by 1 / al: so does c, as far as it may, and the sums keep their size.
+__device__ __forceinline__ void rebase(State& w, int g, int h, float al) {
+  const float c = w.c[g][h];
+  const float n = __uint_as_float(__float_as_uint(fminf(c / al, kMaxC)) & 0x7f800000u);  // al = 0 or NaN: kMaxC
+  const float f = (al * n) / c;  // at most 1
+  w.c[g][h] = n;
+  w.o[g][0][h] *= f;
+  w.o[g][0][2 + h] *= f;
+  w.o[g][1][h] *= f;
+  w.o[g][1][2 + h] *= f;
+}
+
+// bfloat16 number g of two words.
+__device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
+  const uint32_t w = g < 2 ? w01 : w23;
+  return (g & 1) ? bf16_hi(w) : bf16_lo(w);
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+// O += P V for 16 rows whose weights are p (layout of scores); rows outside `ok` weigh nothing.
+__device__ __forceinline__ void weigh(State& w, uint32_t rows, uint32_t row_a, int gid, int tig, const float (&p)[4],
+                                      uint32_t mask, int tok_a) {
+  const uint32_t a = rows + row_a, b = a + 8 * kQ4Row;
+  uint4 ta = lds128(a + kQ4Tail + 16), tb = lds128(b + kQ4Tail + 16);
+  if (mask != 0xffffu) {  // p is 0 there, but 0 times a stray NaN is not
+    if (!((mask >> tok_a) & 1u)) ta = make_uint4(0, 0, 0, 0);
+    if (!((mask >> (tok_a + 8)) & 1u)) tb = make_uint4(0, 0, 0, 0);
+  }
+  uint32_t wa[4], wb[4];
+  __half2 top = __half2half2(__ushort_as_half(0));
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
+    wa[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
+    wb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
+    top = __hmax2(top, __hmax2(as_half2(wa[g]), as_half2(wb[g])));
+  }
+  if (__any_sync(0xffffffffu, __hmax(__low2half(top), __high2half(top)) >= __ushort_as_half(0x7800))) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float c = lower_c(w.c[g][h], fmaxf(p[h] * fa, p[2 + h] * fb)), f = c / w.c[g][h];
+        w.c[g][h] = c;
+        w.o[g][0][h] *= f;
+        w.o[g][0][2 + h] *= f;
+        w.o[g][1][h] *= f;
+        w.o[g][1][2 + h] *= f;
+      }
+      wa[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
+      wb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
+    }
+  }
+  // V rows of this lane's k pairs: fragment rows 2 tig, 2 tig + 1 and those + 8
+  const uint32_t v0 = rows + (uint32_t)tig * kQ4Row + kQ4V + 8 * gid;
+  const uint32_t v1 = rows + (uint32_t)(4 + (tig ^ 2)) * kQ4Row + kQ4V + 8 * gid;
+  const uint2 e0 = lds64(v0), e1 = lds64(v1), e2 = lds64(v0 + 8 * kQ4Row), e3 = lds64(v1 + 8 * kQ4Row);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float za = tail_at(ta.z, ta.w, g), zb = tail_at(tb.z, tb.w, g);
+    w.z[g][0] = fmaf(p[0], za, fmaf(p[2], zb, w.z[g][0]));
+    w.z[g][1] = fmaf(p[1], za, fmaf(p[3], zb, w.z[g][1]));
+    const uint32_t b0 = movmatrix_trans(wa[g]), b1 = movmatrix_trans(wb[g]);
+    const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // half g % 2 of both rows' words
+    uint32_t x = __byte_perm(g < 2 ? e0.x : e0.y, g < 2 ? e1.x : e1.y, sel);
+    uint32_t y = __byte_perm(g < 2 ? e2.x : e2.y, g < 2 ? e3.x : e3.y, sel);
+    mma_f16_16816(w.o[g][0], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
+    x >>= 8;
+    y >>= 8;
+    mma_f16_16816(w.o[g][1], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
+  }
+}
+
+template <bool GATHER, bool F16>
+__global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
+  __shared__ float sm_po[8][kHeadDim], sm_pm[8], sm_pl[8];  // reuse: this block's part for the cluster's merge
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int G = a.G;
   const int64_t bh = (int64_t)b * a.Hkv + h;
+
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * kStages * kStageBytes;
+  const uint32_t bar = smem_u32(&bars[warp][0]);
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
 
   int T = a.seq_len[b];
   bool ok = T >= 0 && T <= a.max_T;
   int n_items = T;
-  const int32_t* rows = nullptr;
+  const int32_t* sel = nullptr;
   if (GATHER && ok) {
     const int am = a.head_map[h];
     ok = am >= 0 && am < a.Hkv;
     if (ok) {
-      rows = a.idx + ((int64_t)b * a.Hkv + am) * a.k_max;
+      sel = a.idx + ((int64_t)b * a.Hkv + am) * a.k_max;
       n_items = a.idx_k[b * a.Hkv + am];
       ok = n_items >= 0 && n_items <= a.k_max;
     }
-    if (T == 0) n_items = 0;
+    if (T == 0) n_items = 0;  // nothing to gather from an empty sequence
   }
   if (!ok) {
     if (threadIdx.x == 0 && split == 0) flag_status(a.status, kStatusBadIndex);
     n_items = 0;
   }
-  const int i_begin = (split * kWarps + warp) * a.tok_per_warp;
-  const int i_end = min((int64_t)i_begin + a.tok_per_warp, (int64_t)n_items);
-
-  float q[G][4];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const uint2 w = *reinterpret_cast<const uint2*>(a.q + ((int64_t)b * a.Hq + h * G + g) * kHeadDim + 4 * lane);
-    unpack2<F16>(w.x, q[g][0], q[g][1]);
-    unpack2<F16>(w.y, q[g][2], q[g][3]);
-  }
-  float m[G], l[G], o[G][4];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-    o[g][0] = o[g][1] = o[g][2] = o[g][3] = 0.f;
-  }
-  const int grp = lane >> 3, r = lane & 7;
+  const int64_t first = (int64_t)(split * kWarps + warp) * a.tok_per_warp;
+  const int i_begin = (int)min(first, (int64_t)n_items);
+  const int i_end = (int)min(first + a.tok_per_warp, (int64_t)n_items);
+  const int n_iter = (i_end - i_begin + kStageRows - 1) / kStageRows;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-  for (int i = i_begin; i < i_end; ++i) {
-    const int t = GATHER ? __ldg(rows + i) : i;
-    int64_t off = -1;
-    if (t >= 0 && t < T) off = q4_row(table, t, a.page_size, a.num_pages, a.Hkv, h);
-    if (off < 0) {
-      if (lane == 0) flag_status(a.status, kStatusBadIndex);
-      if (!GATHER && lane < G) a.logits[(bh * a.max_T + i) * G + lane] = -INFINITY;
-      continue;
+
+  // Row addresses run ahead of the copies: the selected token two stages, its place in the pages one.
+  auto token_of = [&](int it) -> int {
+    const int i = i_begin + kStageRows * it + lane;
+    if (i >= i_end) return -1;
+    if constexpr (GATHER) {
+      const int t = __ldg(sel + i);
+      if (t < 0 || t >= T) flag_status(a.status, kStatusBadIndex);
+      return t < T ? t : -1;  // negative: skipped
+    } else {
+      return i;
     }
-    const uint8_t* row = a.pages + off;
-    const uint32_t kc = *reinterpret_cast<const uint16_t*>(row + 4 * (4 * (r >> 1) + grp) + 2 * (r & 1));
-    const uint32_t vc = *reinterpret_cast<const uint16_t*>(row + kQ4V + 4 * (2 * r + (grp >> 1)) + 2 * (grp & 1));
-    const uint16_t* tail = reinterpret_cast<const uint16_t*>(row + kQ4Tail);
-    const float ks = bf16_lo(tail[grp]), km = bf16_lo(tail[4 + grp]);
-    const float vs = bf16_lo(tail[8 + grp]), vm = bf16_lo(tail[12 + grp]);
+  };
+  auto place_of = [&](int t) -> int64_t {
+    if (t < 0) return -1;
+    const int64_t o = q4_row(table, t, a.page_size, a.num_pages, a.Hkv, h);
+    if (o < 0) flag_status(a.status, kStatusBadIndex);
+    return o;
+  };
+  int token_next = token_of(1);
+  int64_t place_next = place_of(token_of(0));
+  uint32_t masks[kStages];  // rows present, stage by stage in order of use
+  auto issue = [&](int it, int st, uint32_t& mask) {
+    const int64_t place = place_next;
+    place_next = place_of(token_next);
+    token_next = token_of(it + 2);
+    mask = __ballot_sync(0xffffffffu, place >= 0);
+    const uint32_t dst = ring + (uint32_t)st * kStageBytes, br = bar + 8 * st;
+    if (lane == 0) mbar_expect_tx(br, (uint32_t)__popc(mask) * kQ4Row);
+    __syncwarp();
+    if constexpr (GATHER) {
+      if (place >= 0) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + place, kQ4Row, br);
+    } else {
+      // 16 tokens that start at a multiple of 16 lie in one page, one behind the other
+      const uint32_t rows = (uint32_t)__popc((lane < 16 ? mask : mask >> 16) & 0xffffu);
+      if ((lane & 15) == 0 && rows) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + place, rows * kQ4Row, br);
+    }
+  };
+
+  Query qx;
+  load_query<F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
+  State w;
+  w.m0 = w.m1 = -INFINITY;
+  w.l0 = w.l1 = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float s = 0.f;
+  for (int g = 0; g < 4; ++g) {
+    w.z[g][0] = w.z[g][1] = 0.f;
+    w.c[g][0] = w.c[g][1] = kMaxC;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s += q[g][c] * fmaf(ks, (float)((kc >> (4 * c)) & 15u), km);
+    for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
+  }
+  const int tok_a = (gid & 1) ? 4 + ((gid >> 1) ^ 2) : gid >> 1;  // token of fragment row gid
+  const uint32_t row_a = (uint32_t)tok_a * kQ4Row;
+  float* lrow = a.logits + bh * a.max_T * G;
+
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= a.scale_log2;
-      if (!GATHER && lane == 0) a.logits[(bh * a.max_T + i) * G + g] = s;
-      const float mn = fmaxf(m[g], s);
-      const float base = finite_max(mn);
-      const float al = fast_exp2(m[g] - base), p = fast_exp2(s - base);
-      m[g] = mn;
-      l[g] = l[g] * al + p;
+  for (int s = 0; s < kStages - 1; ++s)
+    if (s < n_iter) issue(s, s, masks[s]);
+  int st = 0, phase = 0, st_in = kStages - 1;
+  bool alive = true;
+  int it = 0;
+  for (; it < n_iter; ++it) {
+    if (it + kStages - 1 < n_iter) issue(it + kStages - 1, st_in, masks[kStages - 1]);
+    if (++st_in == kStages) st_in = 0;
+    alive = __all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (uint32_t)phase, a.status));
+    if (!alive) break;
+    const uint32_t rows = ring + (uint32_t)st * kStageBytes;
+    const uint32_t mask = masks[0];
+    const bool two = i_begin + kStageRows * it + 16 < i_end;  // the second 16 rows hold any
+    float s[2][4];
+    scores(qx, rows, row_a, tig, s[0]);
+    if (two) scores(qx, rows + 16 * kQ4Row, row_a, tig, s[1]);
+    else s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
+    if (mask != 0xffffffffu) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[g][c] = o[g][c] * al + p * fmaf(vs, (float)((vc >> (4 * c)) & 15u), vm);
+      for (int u = 0; u < 2; ++u) {
+        if (!((mask >> (16 * u + tok_a)) & 1u)) s[u][0] = s[u][1] = -INFINITY;
+        if (!((mask >> (16 * u + tok_a + 8)) & 1u)) s[u][2] = s[u][3] = -INFINITY;
+      }
+    }
+    if constexpr (!GATHER) {
+      const int t0 = i_begin + kStageRows * it + tok_a;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + 8 * u;
+        const float x0 = s[u >> 1][2 * (u & 1)], x1 = s[u >> 1][2 * (u & 1) + 1];
+        if (t < i_end) {
+          if (2 * tig + 1 < G) *reinterpret_cast<float2*>(lrow + (int64_t)t * G + 2 * tig) = make_float2(x0, x1);
+          else if (2 * tig < G) lrow[(int64_t)t * G + 2 * tig] = x0;
+        }
+      }
+    }
+    const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+    const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+    if (__any_sync(0xffffffffu, x0 > w.m0 + 8.f || x1 > w.m1 + 8.f)) {
+      const float n0 = fmaxf(w.m0, warp_max_xor_gid(x0)), n1 = fmaxf(w.m1, warp_max_xor_gid(x1));
+      const float al0 = fast_exp2(w.m0 - finite_max(n0)), al1 = fast_exp2(w.m1 - finite_max(n1));
+      w.m0 = n0;
+      w.m1 = n1;
+      w.l0 *= al0;
+      w.l1 *= al1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        w.z[g][0] *= al0;
+        w.z[g][1] *= al1;
+        rebase(w, g, 0, al0);
+        rebase(w, g, 1, al1);
+      }
+    }
+    const float base0 = finite_max(w.m0), base1 = finite_max(w.m1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
+      w.l0 += s[u][0] + s[u][2];
+      w.l1 += s[u][1] + s[u][3];
+    }
+    weigh(w, rows, row_a, gid, tig, s[0], mask & 0xffffu, tok_a);
+    if (two) weigh(w, rows + 16 * kQ4Row, row_a, gid, tig, s[1], mask >> 16, tok_a);
+    __syncwarp();  // the stage is read: it may be refilled
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
+    if (++st == kStages) {
+      st = 0;
+      phase ^= 1;
     }
   }
+  if (!alive) {  // gave up on a copy: wait, with the same bound, for the others in flight
+    for (int k = 1; k < kStages && it + k < n_iter; ++k) {
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+      mbar_wait(bar + 8 * st, (uint32_t)phase, a.status);
+    }
+  }
+
+  // ---- merge the four warps; the rings are free once all are here ------------
+  const float l0 = warp_sum_xor_gid(w.l0), l1 = warp_sum_xor_gid(w.l1);
+  __syncthreads();
+  float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
+  if (gid == 0) {
+    sm_m[warp][2 * tig] = w.m0;
+    sm_m[warp][2 * tig + 1] = w.m1;
+    sm_l[warp][2 * tig] = l0;
+    sm_l[warp][2 * tig + 1] = l1;
+  }
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
+  for (int g = 0; g < 4; ++g) {
+    const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^24 / c, every second
+                                                                        // channel in 1/16 of that
+    const float z0 = warp_sum_xor_gid(w.z[g][0]), z1 = warp_sum_xor_gid(w.z[g][1]);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) sm_o[warp][g][4 * lane + c] = o[g][c];
-    if (lane == 0) {
-      sm_m[warp][g] = m[g];
-      sm_l[warp][g] = l[g];
+    for (int u = 0; u < 2; ++u) {
+      const int d = 32 * g + 4 * gid + 2 * u;
+      const float* o = w.o[g][u];
+      *reinterpret_cast<float2*>(&sm_o[warp][2 * tig][d]) =
+          make_float2(fmaf(o[0] * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
+      *reinterpret_cast<float2*>(&sm_o[warp][2 * tig + 1][d]) =
+          make_float2(fmaf(o[1] * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
     }
   }
   __syncthreads();
   const int d = threadIdx.x;  // kThreads == kHeadDim
   for (int g = 0; g < G; ++g) {
     float M = -INFINITY, L = 0.f, acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][g]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = fast_exp2(sm_m[w][g] - finite_max(M));
-      acc += f * sm_o[w][g][d];
-      L += f * sm_l[w][g];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i][g]);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const float f = fast_exp2(sm_m[i][g] - finite_max(M));
+      acc += f * sm_o[i][g][d];
+      L += f * sm_l[i][g];
     }
-    if (GATHER) {
-      a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
-      if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
+    if constexpr (GATHER) {
+      sm_po[g][d] = acc;
+      if (d == 0) {
+        sm_pm[g] = M;
+        sm_pl[g] = L;
+      }
     } else {
       const int64_t slot = (bh * a.nsplit + split) * G + g;
       a.part_o[slot * kHeadDim + d] = acc;
@@ -157,6 +521,27 @@ __global__ void __launch_bounds__(kThreads) decode_q4_kernel(const Q4Args a) {
         a.part_ml[slot * 2 + 1] = L;
       }
     }
+  }
+  if constexpr (GATHER) {
+    // the splits of (b, h) are one cluster: rank 0 merges them through distributed shared memory
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (cluster.block_rank() == 0) {
+      const int ns = (int)cluster.num_blocks();
+      for (int g = 0; g < G; ++g) {
+        float M = -INFINITY, L = 0.f, acc = 0.f;
+        for (int r = 0; r < ns; ++r) M = fmaxf(M, *cluster.map_shared_rank(&sm_pm[g], r));
+        for (int r = 0; r < ns; ++r) {
+          const float f = fast_exp2(*cluster.map_shared_rank(&sm_pm[g], r) - finite_max(M));
+          L += f * *cluster.map_shared_rank(&sm_pl[g], r);
+          acc += f * *cluster.map_shared_rank(&sm_po[g][d], r);
+        }
+        a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
+        if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
+      }
+    }
+    cluster.sync();  // peers keep their shared memory until rank 0 has read it
   }
 }
 
@@ -241,20 +626,12 @@ WsLayout ws_layout(int B, int Hkv, int G, int max_T, int nsplit) {
   return w;
 }
 
-template <bool GATHER, bool F16>
-void launch_g(const Q4Args& a, int G, dim3 grid, cudaStream_t st) {
-  if (G == 1) decode_q4_kernel<1, GATHER, F16><<<grid, kThreads, 0, st>>>(a);
-  else if (G == 2) decode_q4_kernel<2, GATHER, F16><<<grid, kThreads, 0, st>>>(a);
-  else if (G == 4) decode_q4_kernel<4, GATHER, F16><<<grid, kThreads, 0, st>>>(a);
-  else decode_q4_kernel<8, GATHER, F16><<<grid, kThreads, 0, st>>>(a);
-}
-
 Q4Args common_args(const DecodeQ4Params& p) {
   Q4Args a = {};
   a.q = p.q; a.pages = p.kv_pages; a.block_table = p.block_table;
   a.max_pages = p.max_pages; a.page_size = p.page_size; a.num_pages = p.num_pages;
   a.seq_len = p.seq_len; a.idx = p.idx; a.idx_k = p.idx_k; a.head_map = p.head_map; a.k_max = p.k_max;
-  a.Hq = p.Hq; a.Hkv = p.Hkv; a.max_T = p.max_T;
+  a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G; a.max_T = p.max_T;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.out = p.out; a.lse = p.lse; a.status = p.status;
   return a;
@@ -277,10 +654,11 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   const dim3 grid(sp.nsplit, p.Hkv, p.B);
-  if (p.f16) launch_g<false, true>(a, p.G, grid, st);
-  else launch_g<false, false>(a, p.G, grid, st);
-  const cudaError_t e = cudaGetLastError();
+  auto kern = p.f16 ? decode_q4_kernel<false, true> : decode_q4_kernel<false, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, kSmemBytes, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   CombineArgs c;
   c.seq_len = p.seq_len;
   c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.nsplit = sp.nsplit;
@@ -293,12 +671,31 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
 }
 
 cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st) {
+  const DecodeSplit sp = decode_split_for(p.B * p.Hkv, p.k_max, true);
   Q4Args a = common_args(p);
-  a.nsplit = 1;
-  a.tok_per_warp = (p.k_max + kWarps - 1) / kWarps;
-  const dim3 grid(1, p.Hkv, p.B);
-  if (p.f16) launch_g<true, true>(a, p.G, grid, st);
-  else launch_g<true, false>(a, p.G, grid, st);
+  a.tok_per_warp = sp.tok_per_warp;
+  a.nsplit = sp.nsplit;
+  auto kern = p.f16 ? decode_q4_kernel<true, true> : decode_q4_kernel<true, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  if (sp.nsplit > 8) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sp.nsplit, p.Hkv, p.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = sp.nsplit;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

@@ -402,10 +402,12 @@ int kascade_qk_norm_rope_f16(kascade_shape s, int32_t N, const uint16_t* q, kasc
 
 // ------------------------------------------------------ 4-bit paged cache --
 static int check_pages_q4(const uint8_t* kv_pages, const int32_t* block_table, int32_t num_pages, int32_t max_pages,
-                          int32_t page_size) {
+                          int32_t page_size, int32_t Hkv) {
   if (!kv_pages || !block_table || num_pages < 1 || max_pages < 1 || page_size < 16 || (page_size % 16))
     return KASCADE_ERR_INVALID_ARG;
   if (!aligned16(kv_pages) || ((uintptr_t)block_table & 3)) return KASCADE_ERR_INVALID_ARG;
+  // rows of the store are counted in 32 bits
+  if ((int64_t)num_pages * Hkv > INT32_MAX / page_size) return KASCADE_ERR_UNSUPPORTED_SHAPE;
   return KASCADE_OK;
 }
 
@@ -422,7 +424,7 @@ static int kv_write_paged_q4_impl(kascade_shape s, int32_t N, const uint16_t* k,
                                   const int32_t* start, const int32_t* count, void* stream, bool f16) {
   int rc = check_cache_shape(s, N);
   if (rc || s.B == 0 || N == 0) return rc;
-  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size, s.Hkv))) return rc;
   if (!k || !v || !start || !aligned16(k) || !aligned16(v) || ((uintptr_t)start & 3) || ((uintptr_t)count & 3) ||
       !strides_ok(k_strides) || !strides_ok(v_strides))
     return KASCADE_ERR_INVALID_ARG;
@@ -459,7 +461,7 @@ static int kv_read_paged_q4_impl(kascade_shape s, int32_t N, const uint8_t* kv_p
                                  bool f16) {
   int rc = check_cache_shape(s, N);
   if (rc || s.B == 0 || N == 0) return rc;
-  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size, s.Hkv))) return rc;
   if (!k || !v || k == v || !start || !aligned16(k) || !aligned16(v) || ((uintptr_t)start & 3) ||
       ((uintptr_t)count & 3))
     return KASCADE_ERR_INVALID_ARG;
@@ -504,7 +506,7 @@ static int decode_anchor_paged_q4_impl(kascade_shape s, const uint16_t* q, const
   if (max_T > kMaxRowLen || decode_logits_too_large(s, max_T) || s.B > 65535 || s.Hkv > 65535)
     return KASCADE_ERR_UNSUPPORTED_SHAPE;
   if (s.B == 0) return KASCADE_OK;
-  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size, s.Hkv))) return rc;
   if ((int64_t)max_pages * page_size < max_T) return KASCADE_ERR_INVALID_ARG;
   if (!q || !seq_len || !out || (max_T > 0 && !pooled) || !ws) return KASCADE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(pooled) || !aligned16(ws) || !aligned16(lse) ||
@@ -549,7 +551,7 @@ static int decode_reuse_paged_q4_impl(kascade_shape s, const uint16_t* q, const 
   if (k_max < 0 || !std::isfinite(scale)) return KASCADE_ERR_INVALID_ARG;
   if (k_max > kMaxRowLen || s.B > 65535 || s.Hkv > 65535) return KASCADE_ERR_UNSUPPORTED_SHAPE;
   if (s.B == 0) return KASCADE_OK;
-  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size))) return rc;
+  if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size, s.Hkv))) return rc;
   if (!q || !seq_len || (k_max > 0 && !idx) || !idx_k || !head_map || !out) return KASCADE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || ((uintptr_t)seq_len & 3) || ((uintptr_t)idx & 3) ||
       ((uintptr_t)idx_k & 3) || ((uintptr_t)head_map & 3))

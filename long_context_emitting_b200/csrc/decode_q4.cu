@@ -53,6 +53,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+#ifndef Q4_MAX_TPW
+#define Q4_MAX_TPW 512
+#endif
 constexpr int kStageRows = 32;
 constexpr int kStages = 2;
 constexpr uint32_t kStageBytes = kStageRows * kQ4Row;
@@ -66,13 +69,14 @@ struct Q4Args {
   const uint8_t* pages;
   const int32_t* block_table;
   int max_pages, page_size, num_pages;
+  uint32_t page_mul, page_shift;  // t / page_size = umulhi(t, page_mul) >> page_shift, 0 <= t < 2^31
   const int32_t* seq_len;
   const int32_t* idx;
   const int32_t* idx_k;
   const int32_t* head_map;
   int k_max;
   int Hq, Hkv, G, max_T;
-  int tok_per_warp, nsplit;  // tok_per_warp is a multiple of 16
+  int tok_per_warp, nsplit;  // tok_per_warp is a multiple of 32
   float scale_log2;
   float* logits;   // anchor: [B, Hkv, max_T, G] base-2 scaled logits
   float* part_ml;  // [B*Hkv, nsplit, G, 2]
@@ -111,15 +115,16 @@ struct Query {
   float f0, f1;       // factors of heads 2 tig, 2 tig + 1 to base-2 logits
 };
 
-template <bool F16>
+template <bool PAIR, bool F16>
 __device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, float scale_log2, int gid, int tig) {
   float v[4][8];
   float top = 0.f;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    // columns gid >= G are padding: load a valid row and zero it
-    uint4 w = ldg16(q + (gid < G ? gid : G - 1) * kHeadDim + 32 * g + 8 * tig);
-    if (gid >= G) w = make_uint4(0, 0, 0, 0);
+    // columns past the last head are padding: load a valid row and zero it
+    const int head = PAIR ? gid & 3 : gid;
+    uint4 w = ldg16(q + (head < G ? head : G - 1) * kHeadDim + 32 * g + 8 * tig);
+    if (head >= G) w = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       unpack2<F16>(word_of(w, i), v[g][2 * i], v[g][2 * i + 1]);
@@ -193,7 +198,7 @@ __device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t r
   s[3] = c[3] * 0x1p24f * x.f1;
 }
 
-// Running state of a warp: heads 2 tig, 2 tig + 1.
+// Running state of a warp.  A lane's heads are 2 tig, 2 tig + 1 (PAIR: 2 (tig & 1) and the next).
 struct State {
   float m0, m1, l0, l1;
   float o[4][2][4];  // [group][channel pair]: rows gid = channel 4 gid + 2 pair, gid + 8 = the next (times 16)
@@ -201,27 +206,43 @@ struct State {
   float c[4][2];     // [group][head]: the sums o and the weights that enter them are times this power of two
 };
 
-constexpr float kMaxC = 0x1p100f;
+constexpr int kMaxC = 127 + 100;  // largest c that a sum starts from, 2^100, as a biased exponent
 
-// A weight has reached 2^15: new factors, which put the largest weight of each head and group that
-// did so in [2^7, 2^8).  x: p · vs / c of the lane's rows (not finite: it spoils its own sum only).
-__device__ __noinline__ float lower_c(float c, float x) {
-  x = x < INFINITY ? x : 0.f;
-  x = warp_max_xor_gid(x);
-  const int e = max((int)(__float_as_uint(x) >> 23), 27);  // biased; c stays within 2^107
-  return x * c < 0x1p15f ? c : __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23);
+// Over the lanes that hold the same head (tig), with PAIR also those of the other 16 rows.
+template <bool PAIR>
+__device__ __forceinline__ float head_max(float x) {
+  if constexpr (PAIR) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  return warp_max_xor_gid(x);
+}
+template <bool PAIR>
+__device__ __forceinline__ float head_sum(float x) {
+  if constexpr (PAIR) x += __shfl_xor_sync(0xffffffffu, x, 2);
+  return warp_sum_xor_gid(x);
 }
 
-// The weights' unit grows by 1 / al: so does c, as far as it may, and the sums keep their size.
-__device__ __forceinline__ void rebase(State& w, int g, int h, float al) {
-  const float c = w.c[g][h];
-  const float n = __uint_as_float(__float_as_uint(fminf(c / al, kMaxC)) & 0x7f800000u);  // al = 0 or NaN: kMaxC
-  const float f = (al * n) / c;  // at most 1
-  w.c[g][h] = n;
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23); }  // x >= 0
+__device__ __forceinline__ float biased_pow2(int e) { return __int_as_float(max(e, 0) << 23); }
+
+__device__ __forceinline__ void scale_sums(State& w, int g, int h, float f) {
   w.o[g][0][h] *= f;
   w.o[g][0][2 + h] *= f;
   w.o[g][1][h] *= f;
   w.o[g][1][2 + h] *= f;
+}
+
+// The weights' unit of head h has grown by 1 / al, 0 <= al <= 1 (NaN: the head is lost anyway): c
+// takes up the power of two, as far as it may, and the sums what is left.
+__device__ __forceinline__ void rebase(State& w, int h, float al) {
+  const bool some = al > 0.f;
+  const int up = some ? 127 - exponent_of(al) : 512;
+  const float rest = some ? __uint_as_float((__float_as_uint(al) & 0x7fffffu) | 0x3f800000u) : 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int e = exponent_of(w.c[g][h]) + up, n = min(e, kMaxC);
+    w.c[g][h] = biased_pow2(n);
+    scale_sums(w, g, h, rest * biased_pow2(127 + n - e));
+    w.z[g][h] *= al;
+  }
 }
 
 // bfloat16 number g of two words.
@@ -232,62 +253,77 @@ __device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
-// O += P V for 16 rows whose weights are p (layout of scores); rows outside `ok` weigh nothing.
-__device__ __forceinline__ void weigh(State& w, uint32_t rows, uint32_t row_a, int gid, int tig, const float (&p)[4],
-                                      uint32_t mask, int tok_a) {
-  const uint32_t a = rows + row_a, b = a + 8 * kQ4Row;
-  uint4 ta = lds128(a + kQ4Tail + 16), tb = lds128(b + kQ4Tail + 16);
+// Weights p · vs · c of this lane's rows a and b (layout of scores) as the B operands of the value
+// products, and the minima's sums.  `tail` is the address of row a's V scales.
+template <bool PAIR>
+__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], uint32_t mask, int tok_a,
+                                        uint32_t (&ba)[4], uint32_t (&bb)[4]) {
+  uint4 ta = lds128(tail), tb = lds128(tail + 8 * kQ4Row);
   if (mask != 0xffffu) {  // p is 0 there, but 0 times a stray NaN is not
     if (!((mask >> tok_a) & 1u)) ta = make_uint4(0, 0, 0, 0);
     if (!((mask >> (tok_a + 8)) & 1u)) tb = make_uint4(0, 0, 0, 0);
   }
-  uint32_t wa[4], wb[4];
-  __half2 top = __half2half2(__ushort_as_half(0));
+  __half2 top = as_half2(0);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
-    wa[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
-    wb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
-    top = __hmax2(top, __hmax2(as_half2(wa[g]), as_half2(wb[g])));
+    ba[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
+    bb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
+    top = __hmax2(top, __hmax2(as_half2(ba[g]), as_half2(bb[g])));
   }
   if (__any_sync(0xffffffffu, __hmax(__low2half(top), __high2half(top)) >= __ushort_as_half(0x7800))) {
+    // A weight has reached 2^15: factors that put the largest weight of such a head and group in
+    // [2^7, 2^8).  A weight that is not finite spoils its own sums and moves no factor.
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float c = lower_c(w.c[g][h], fmaxf(p[h] * fa, p[2 + h] * fb)), f = c / w.c[g][h];
-        w.c[g][h] = c;
-        w.o[g][0][h] *= f;
-        w.o[g][0][2 + h] *= f;
-        w.o[g][1][h] *= f;
-        w.o[g][1][2 + h] *= f;
+        const float xa = p[h] * fa, xb = p[2 + h] * fb;
+        const float x = head_max<PAIR>(fmaxf(xa < INFINITY ? xa : 0.f, xb < INFINITY ? xb : 0.f));
+        if (x * w.c[g][h] >= 0x1p15f) {
+          const int n = 127 + 7 + 127 - max(exponent_of(x), 27);  // c stays within 2^107
+          scale_sums(w, g, h, biased_pow2(127 + n - exponent_of(w.c[g][h])));
+          w.c[g][h] = biased_pow2(n);
+        }
       }
-      wa[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
-      wb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
+      ba[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
+      bb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
     }
   }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float za = tail_at(ta.z, ta.w, g), zb = tail_at(tb.z, tb.w, g);
+    w.z[g][0] = fmaf(p[0], za, fmaf(p[2], zb, w.z[g][0]));
+    w.z[g][1] = fmaf(p[1], za, fmaf(p[3], zb, w.z[g][1]));
+    ba[g] = movmatrix_trans(ba[g]);
+    bb[g] = movmatrix_trans(bb[g]);
+  }
+}
+
+// O += V P for the 16 rows at `rows`.
+__device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig, const uint32_t (&ba)[4],
+                                       const uint32_t (&bb)[4]) {
   // V rows of this lane's k pairs: fragment rows 2 tig, 2 tig + 1 and those + 8
   const uint32_t v0 = rows + (uint32_t)tig * kQ4Row + kQ4V + 8 * gid;
   const uint32_t v1 = rows + (uint32_t)(4 + (tig ^ 2)) * kQ4Row + kQ4V + 8 * gid;
   const uint2 e0 = lds64(v0), e1 = lds64(v1), e2 = lds64(v0 + 8 * kQ4Row), e3 = lds64(v1 + 8 * kQ4Row);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const float za = tail_at(ta.z, ta.w, g), zb = tail_at(tb.z, tb.w, g);
-    w.z[g][0] = fmaf(p[0], za, fmaf(p[2], zb, w.z[g][0]));
-    w.z[g][1] = fmaf(p[1], za, fmaf(p[3], zb, w.z[g][1]));
-    const uint32_t b0 = movmatrix_trans(wa[g]), b1 = movmatrix_trans(wb[g]);
     const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // half g % 2 of both rows' words
     uint32_t x = __byte_perm(g < 2 ? e0.x : e0.y, g < 2 ? e1.x : e1.y, sel);
     uint32_t y = __byte_perm(g < 2 ? e2.x : e2.y, g < 2 ? e3.x : e3.y, sel);
-    mma_f16_16816(w.o[g][0], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
+    mma_f16_16816(w.o[g][0], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ba[g], bb[g]);
     x >>= 8;
     y >>= 8;
-    mma_f16_16816(w.o[g][1], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
+    mma_f16_16816(w.o[g][1], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ba[g], bb[g]);
   }
 }
 
-template <bool GATHER, bool F16>
+// PAIR: at most 4 query heads per key head.  They are in columns 0..3 and again in 4..7, and after
+// the scores the lanes of columns 4..7 work on the second 16 rows of a stage: exponentials, weights
+// and minima then cost half.
+template <bool GATHER, bool PAIR, bool F16>
 __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
@@ -328,9 +364,13 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
     if (threadIdx.x == 0 && split == 0) flag_status(a.status, kStatusBadIndex);
     n_items = 0;
   }
-  const int64_t first = (int64_t)(split * kWarps + warp) * a.tok_per_warp;
+  // A reuse row is shared out evenly over the cluster's warps, whatever its length.
+  const int tok_per_warp =
+      GATHER ? ((n_items + a.nsplit * kWarps - 1) / (a.nsplit * kWarps) + 31) & ~31 : a.tok_per_warp;
+  if (!GATHER && (int64_t)split * kWarps * tok_per_warp >= n_items) return;  // the combine kernel skips this part
+  const int64_t first = (int64_t)(split * kWarps + warp) * tok_per_warp;
   const int i_begin = (int)min(first, (int64_t)n_items);
-  const int i_end = (int)min(first + a.tok_per_warp, (int64_t)n_items);
+  const int i_end = (int)min(first + tok_per_warp, (int64_t)n_items);
   const int n_iter = (i_end - i_begin + kStageRows - 1) / kStageRows;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
@@ -346,41 +386,53 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
       return i;
     }
   };
-  auto place_of = [&](int t) -> int64_t {
+  auto place_of = [&](int t) -> int {  // row of the page store, or -1
     if (t < 0) return -1;
-    const int64_t o = q4_row(table, t, a.page_size, a.num_pages, a.Hkv, h);
-    if (o < 0) flag_status(a.status, kStatusBadIndex);
-    return o;
+    const int pi = (int)(__umulhi((uint32_t)t, a.page_mul) >> a.page_shift);
+    const int page = __ldg(table + pi);
+    if ((unsigned)page >= (unsigned)a.num_pages) {
+      flag_status(a.status, kStatusBadIndex);
+      return -1;
+    }
+    return (page * a.Hkv + h) * a.page_size + (t - pi * a.page_size);
   };
   int token_next = token_of(1);
-  int64_t place_next = place_of(token_of(0));
+  int place_next = place_of(token_of(0));
   uint32_t masks[kStages];  // rows present, stage by stage in order of use
   auto issue = [&](int it, int st, uint32_t& mask) {
-    const int64_t place = place_next;
+    const int place = place_next;
     place_next = place_of(token_next);
     token_next = token_of(it + 2);
     mask = __ballot_sync(0xffffffffu, place >= 0);
     const uint32_t dst = ring + (uint32_t)st * kStageBytes, br = bar + 8 * st;
-    if (lane == 0) mbar_expect_tx(br, (uint32_t)__popc(mask) * kQ4Row);
-    __syncwarp();
     if constexpr (GATHER) {
-      if (place >= 0) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + place, kQ4Row, br);
+      // 320 chunks of 16 bytes, ten to a row; the two of a 32-byte sector go to neighbouring lanes
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        const int u = lane + 2 * i, r = (u * 205) >> 11;  // (lane + 32 i) / 10 = r + 3 i
+        const int pl = __shfl_sync(0xffffffffu, place, r + 3 * i);
+        cp_async16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
+                   pl >= 0 ? 16 : 0);
+      }
     } else {
+      if (lane == 0) mbar_expect_tx(br, (uint32_t)__popc(mask) * kQ4Row);
+      __syncwarp();
       // 16 tokens that start at a multiple of 16 lie in one page, one behind the other
       const uint32_t rows = (uint32_t)__popc((lane < 16 ? mask : mask >> 16) & 0xffffu);
-      if ((lane & 15) == 0 && rows) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + place, rows * kQ4Row, br);
+      if ((lane & 15) == 0 && rows)
+        bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, rows * kQ4Row, br);
     }
   };
 
   Query qx;
-  load_query<F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
+  load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
   State w;
   w.m0 = w.m1 = -INFINITY;
   w.l0 = w.l1 = 0.f;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     w.z[g][0] = w.z[g][1] = 0.f;
-    w.c[g][0] = w.c[g][1] = kMaxC;
+    w.c[g][0] = w.c[g][1] = biased_pow2(kMaxC);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
   }
@@ -388,70 +440,97 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
   const uint32_t row_a = (uint32_t)tok_a * kQ4Row;
   float* lrow = a.logits + bh * a.max_T * G;
 
+  // PAIR: this lane's rows of a stage are the first 16 or, from tig 2 on, the second
+  const uint32_t half = PAIR && tig >= 2 ? 16 : 0;
+  const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
+
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
+  for (int s = 0; s < kStages - 1; ++s) {
     if (s < n_iter) issue(s, s, masks[s]);
+    if constexpr (GATHER) cp_async_commit();
+  }
   int st = 0, phase = 0, st_in = kStages - 1;
   bool alive = true;
   int it = 0;
   for (; it < n_iter; ++it) {
     if (it + kStages - 1 < n_iter) issue(it + kStages - 1, st_in, masks[kStages - 1]);
     if (++st_in == kStages) st_in = 0;
-    alive = __all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (uint32_t)phase, a.status));
-    if (!alive) break;
+    if constexpr (GATHER) {
+      cp_async_commit();
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+    } else {
+      alive = __all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (uint32_t)phase, a.status));
+      if (!alive) break;
+    }
     const uint32_t rows = ring + (uint32_t)st * kStageBytes;
     const uint32_t mask = masks[0];
-    const bool two = i_begin + kStageRows * it + 16 < i_end;  // the second 16 rows hold any
+    constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
     float s[2][4];
     scores(qx, rows, row_a, tig, s[0]);
-    if (two) scores(qx, rows + 16 * kQ4Row, row_a, tig, s[1]);
-    else s[1][0] = s[1][1] = s[1][2] = s[1][3] = -INFINITY;
+    scores(qx, rows + 16 * kQ4Row, row_a, tig, s[1]);
+    if constexpr (PAIR) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[0][i] = half ? s[1][i] : s[0][i];
+    }
     if (mask != 0xffffffffu) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (!((mask >> (16 * u + tok_a)) & 1u)) s[u][0] = s[u][1] = -INFINITY;
-        if (!((mask >> (16 * u + tok_a + 8)) & 1u)) s[u][2] = s[u][3] = -INFINITY;
+      for (int u = 0; u < kSets; ++u) {
+        if (!((mask >> (16 * u + half + tok_a)) & 1u)) s[u][0] = s[u][1] = -INFINITY;
+        if (!((mask >> (16 * u + half + tok_a + 8)) & 1u)) s[u][2] = s[u][3] = -INFINITY;
       }
     }
     if constexpr (!GATHER) {
-      const int t0 = i_begin + kStageRows * it + tok_a;
+      const int t0 = i_begin + kStageRows * it + (int)half + tok_a;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2 * kSets; ++u) {
         const int t = t0 + 8 * u;
         const float x0 = s[u >> 1][2 * (u & 1)], x1 = s[u >> 1][2 * (u & 1) + 1];
         if (t < i_end) {
-          if (2 * tig + 1 < G) *reinterpret_cast<float2*>(lrow + (int64_t)t * G + 2 * tig) = make_float2(x0, x1);
-          else if (2 * tig < G) lrow[(int64_t)t * G + 2 * tig] = x0;
+          if (!(G & 1) && col < G) *reinterpret_cast<float2*>(lrow + (int64_t)t * G + col) = make_float2(x0, x1);
+          else if (col < G) {
+            lrow[(int64_t)t * G + col] = x0;
+            if (col + 1 < G) lrow[(int64_t)t * G + col + 1] = x1;
+          }
         }
       }
     }
-    const float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-    const float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+    if constexpr (!PAIR) {
+      x0 = fmaxf(x0, fmaxf(s[1][0], s[1][2]));
+      x1 = fmaxf(x1, fmaxf(s[1][1], s[1][3]));
+    }
     if (__any_sync(0xffffffffu, x0 > w.m0 + 8.f || x1 > w.m1 + 8.f)) {
-      const float n0 = fmaxf(w.m0, warp_max_xor_gid(x0)), n1 = fmaxf(w.m1, warp_max_xor_gid(x1));
+      const float n0 = fmaxf(w.m0, head_max<PAIR>(x0)), n1 = fmaxf(w.m1, head_max<PAIR>(x1));
       const float al0 = fast_exp2(w.m0 - finite_max(n0)), al1 = fast_exp2(w.m1 - finite_max(n1));
       w.m0 = n0;
       w.m1 = n1;
       w.l0 *= al0;
       w.l1 *= al1;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        w.z[g][0] *= al0;
-        w.z[g][1] *= al1;
-        rebase(w, g, 0, al0);
-        rebase(w, g, 1, al1);
-      }
+      rebase(w, 0, al0);
+      rebase(w, 1, al1);
     }
     const float base0 = finite_max(w.m0), base1 = finite_max(w.m1);
+    uint32_t ba[4], bb[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kSets; ++u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
       w.l0 += s[u][0] + s[u][2];
       w.l1 += s[u][1] + s[u][3];
+      weights<PAIR>(w, rows + (16 * u + half) * kQ4Row + row_a + kQ4Tail + 16, s[u], (mask >> (16 * u + half)) & 0xffffu,
+                    tok_a, ba, bb);
+      values(w, rows + 16 * u * kQ4Row, gid, tig, ba, bb);
     }
-    weigh(w, rows, row_a, gid, tig, s[0], mask & 0xffffu, tok_a);
-    if (two) weigh(w, rows + 16 * kQ4Row, row_a, gid, tig, s[1], mask >> 16, tok_a);
+    if constexpr (PAIR) {
+      // the second rows' weights stand in columns 4..7: swap them to 0..3 (4..7 of the sums are not used)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        ba[g] = __shfl_xor_sync(0xffffffffu, ba[g], 16);
+        bb[g] = __shfl_xor_sync(0xffffffffu, bb[g], 16);
+      }
+      values(w, rows + 16 * kQ4Row, gid, tig, ba, bb);
+    }
     __syncwarp();  // the stage is read: it may be refilled
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
@@ -471,27 +550,29 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
   }
 
   // ---- merge the four warps; the rings are free once all are here ------------
-  const float l0 = warp_sum_xor_gid(w.l0), l1 = warp_sum_xor_gid(w.l1);
+  const float l0 = head_sum<PAIR>(w.l0), l1 = head_sum<PAIR>(w.l1);
   __syncthreads();
   float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
-  if (gid == 0) {
-    sm_m[warp][2 * tig] = w.m0;
-    sm_m[warp][2 * tig + 1] = w.m1;
-    sm_l[warp][2 * tig] = l0;
-    sm_l[warp][2 * tig + 1] = l1;
+  const bool owner = !PAIR || tig < 2;
+  if (gid == 0 && owner) {
+    sm_m[warp][col] = w.m0;
+    sm_m[warp][col + 1] = w.m1;
+    sm_l[warp][col] = l0;
+    sm_l[warp][col + 1] = l1;
   }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^24 / c, every second
                                                                         // channel in 1/16 of that
-    const float z0 = warp_sum_xor_gid(w.z[g][0]), z1 = warp_sum_xor_gid(w.z[g][1]);
+    const float z0 = head_sum<PAIR>(w.z[g][0]), z1 = head_sum<PAIR>(w.z[g][1]);
+    if (!owner) continue;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int d = 32 * g + 4 * gid + 2 * u;
       const float* o = w.o[g][u];
-      *reinterpret_cast<float2*>(&sm_o[warp][2 * tig][d]) =
+      *reinterpret_cast<float2*>(&sm_o[warp][col][d]) =
           make_float2(fmaf(o[0] * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
-      *reinterpret_cast<float2*>(&sm_o[warp][2 * tig + 1][d]) =
+      *reinterpret_cast<float2*>(&sm_o[warp][col + 1][d]) =
           make_float2(fmaf(o[1] * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
     }
   }
@@ -547,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
 
 struct CombineArgs {
   const int32_t* seq_len;
-  int Hq, Hkv, G, max_T, nsplit;
+  int Hq, Hkv, G, max_T, nsplit, per_split;  // per_split: tokens of a split
   const float* part_ml;
   const float* part_o;
   const float* logits;
@@ -558,54 +639,84 @@ struct CombineArgs {
 };
 
 constexpr int kCombineThreads = 256;
-constexpr int kPoolChunk = 2048;  // tokens per block
+constexpr int kPoolChunk = 1024;  // tokens per block
 
-// Second kernel of the anchor: every block merges the splits' maxima and sums of its (b, h); the
-// first also their outputs; each turns its chunk of logits into pooled probabilities.
+// Second kernel of the anchor.  Blocks x < G merge the outputs of one head over the splits, eight
+// splits at a time; the others turn a chunk of logits into pooled probabilities.  Each works out the
+// maxima and sums that it needs from the splits'.
 template <bool F16>
 __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(const CombineArgs a) {
   __shared__ float s_M[8], s_L[8], s_lse2[8];
-  const int b = blockIdx.z, h = blockIdx.y, chunk = blockIdx.x;
+  __shared__ float4 s_o[kCombineThreads / 32][kHeadDim / 4];
+  const int b = blockIdx.z, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G;
   const int64_t bh = (int64_t)b * a.Hkv + h;
+  int T = a.seq_len[b];
+  if (T < 0 || T > a.max_T) T = 0;
+  const bool merge = blockIdx.x < G;
+  const int chunk = (int)blockIdx.x - G;
+  if (!merge && (int64_t)chunk * kPoolChunk >= T) return;
+  const int ns = (T + a.per_split - 1) / a.per_split;  // splits that hold tokens
   const float* ml = a.part_ml + bh * a.nsplit * G * 2;
-  if (warp < G) {
+  if (merge ? warp == 0 : warp < G) {
+    const int g = merge ? (int)blockIdx.x : warp;
     float M = -INFINITY, L = 0.f;
-    for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, ml[(s * G + warp) * 2]);
+    for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[(s * G + g) * 2]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int s = lane; s < a.nsplit; s += 32)
-      L += fast_exp2(ml[(s * G + warp) * 2] - finite_max(M)) * ml[(s * G + warp) * 2 + 1];
+    for (int s = lane; s < ns; s += 32) L += fast_exp2(ml[(s * G + g) * 2] - finite_max(M)) * ml[(s * G + g) * 2 + 1];
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) {
-      s_M[warp] = finite_max(M);
-      s_L[warp] = L;
-      s_lse2[warp] = lse2_of(M, L);
+      s_M[g] = finite_max(M);
+      s_L[g] = L;
+      s_lse2[g] = lse2_of(M, L);
     }
   }
   __syncthreads();
-  if (chunk == 0) {
-    const float* po = a.part_o + bh * a.nsplit * G * kHeadDim;
-    for (int e = threadIdx.x; e < G * kHeadDim; e += kCombineThreads) {
-      const int g = e / kHeadDim, d = e % kHeadDim;
-      float acc = 0.f;
-      for (int s = 0; s < a.nsplit; ++s)
-        acc += fast_exp2(ml[(s * G + g) * 2] - s_M[g]) * po[((int64_t)s * G + g) * kHeadDim + d];
-      a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(s_L[g] == 0.f ? 0.f : acc / s_L[g]);
+  if (merge) {
+    const int g = (int)blockIdx.x;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + bh * a.nsplit * G * kHeadDim) + g * 32 + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = warp; s < ns; s += kCombineThreads / 32) {
+      const float f = fast_exp2(ml[(s * G + g) * 2] - s_M[g]);
+      const float4 v = po[(int64_t)s * G * 32];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
     }
-    if (a.lse && threadIdx.x < G) a.lse[(int64_t)b * a.Hq + h * G + threadIdx.x] = s_lse2[threadIdx.x] * kLn2;
+    s_o[warp][lane] = acc;
+    __syncthreads();
+    if (threadIdx.x < kHeadDim) {
+      float o = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCombineThreads / 32; ++i) o += reinterpret_cast<const float*>(s_o[i])[threadIdx.x];
+      a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + threadIdx.x] = to_bits<F16>(s_L[g] == 0.f ? 0.f : o / s_L[g]);
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = s_lse2[g] * kLn2;
+    return;
   }
-  int T = a.seq_len[b];
-  if (T < 0 || T > a.max_T) T = 0;
   const int t_hi = (int)min((int64_t)(chunk + 1) * kPoolChunk, (int64_t)T);
   const float* lrow = a.logits + bh * a.max_T * G;
   float* prow = a.pooled + bh * a.ld_pooled;
   const float invG = 1.f / (float)G;
+  // no finite score at all (every page entry bad): relative to 0 the probabilities are 0
+  if (G == 4) {
+    float x[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) x[g] = finite_max(s_lse2[g]);
+#pragma unroll 4
+    for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
+      const float4 v = reinterpret_cast<const float4*>(lrow)[t];
+      prow[t] = 0.25f * (fast_exp2(v.x - x[0]) + fast_exp2(v.y - x[1]) + fast_exp2(v.z - x[2]) + fast_exp2(v.w - x[3]));
+    }
+    return;
+  }
   for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
     float acc = 0.f;
-    // no finite score at all (every page entry bad): relative to 0 the probabilities are 0
     for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - finite_max(s_lse2[g]));
     prow[t] = acc * invG;
   }
@@ -626,10 +737,29 @@ WsLayout ws_layout(int B, int Hkv, int G, int max_T, int nsplit) {
   return w;
 }
 
+// Work split of `units` (sequence, key head) rows of up to n_items tokens.
+DecodeSplit q4_split(int units, int n_items, bool gather) {
+  constexpr int kSlots = 4 * 148;  // resident blocks
+  DecodeSplit s;
+  int64_t nsplit = units >= kSlots ? 1 : kSlots / units;  // one wave
+  if (gather && nsplit > 16) nsplit = 16;                 // the splits of a row are one cluster
+  const int64_t per = kWarps * nsplit;
+  int64_t tpw = ((n_items + per - 1) / per + 31) / 32 * 32;
+  if (tpw < 32) tpw = 32;
+  if (!gather && tpw > Q4_MAX_TPW) tpw = Q4_MAX_TPW;
+  s.tok_per_warp = (int)tpw;
+  s.nsplit = n_items > 0 ? (int)((n_items + kWarps * tpw - 1) / (kWarps * tpw)) : 1;
+  return s;
+}
+
 Q4Args common_args(const DecodeQ4Params& p) {
   Q4Args a = {};
   a.q = p.q; a.pages = p.kv_pages; a.block_table = p.block_table;
   a.max_pages = p.max_pages; a.page_size = p.page_size; a.num_pages = p.num_pages;
+  // with 2^(s+1) >= page_size > 2^s and mul = floor(2^(32+s) / page_size) + 1 the product is too
+  // large by at most t 2^(s+1) < 2^(32+s): never enough to reach the next quotient
+  while (((int64_t)2 << a.page_shift) < p.page_size) ++a.page_shift;
+  a.page_mul = (uint32_t)(((uint64_t)1 << (32 + a.page_shift)) / (uint64_t)p.page_size + 1);
   a.seq_len = p.seq_len; a.idx = p.idx; a.idx_k = p.idx_k; a.head_map = p.head_map; a.k_max = p.k_max;
   a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G; a.max_T = p.max_T;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
@@ -637,14 +767,20 @@ Q4Args common_args(const DecodeQ4Params& p) {
   return a;
 }
 
+template <bool GATHER>
+auto pick_kernel(bool pair, bool f16) {
+  return pair ? (f16 ? decode_q4_kernel<GATHER, true, true> : decode_q4_kernel<GATHER, true, false>)
+              : (f16 ? decode_q4_kernel<GATHER, false, true> : decode_q4_kernel<GATHER, false, false>);
+}
+
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int B, int Hkv, int G, int max_T) {
-  return ws_layout(B, Hkv, G, max_T, decode_split_for(B * Hkv, max_T, false).nsplit).total;
+  return ws_layout(B, Hkv, G, max_T, q4_split(B * Hkv, max_T, false).nsplit).total;
 }
 
 cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
-  const DecodeSplit sp = decode_split_for(p.B * p.Hkv, p.max_T, false);
+  const DecodeSplit sp = q4_split(p.B * p.Hkv, p.max_T, false);
   const WsLayout w = ws_layout(p.B, p.Hkv, p.G, p.max_T, sp.nsplit);
   char* ws = static_cast<char*>(p.ws);
   Q4Args a = common_args(p);
@@ -654,7 +790,7 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   const dim3 grid(sp.nsplit, p.Hkv, p.B);
-  auto kern = p.f16 ? decode_q4_kernel<false, true> : decode_q4_kernel<false, false>;
+  auto kern = pick_kernel<false>(p.G <= 4, p.f16);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, kSmemBytes, st>>>(a);
@@ -662,20 +798,21 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   CombineArgs c;
   c.seq_len = p.seq_len;
   c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.nsplit = sp.nsplit;
+  c.per_split = kWarps * sp.tok_per_warp;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
-  const dim3 cgrid(p.max_T > 0 ? (p.max_T + kPoolChunk - 1) / kPoolChunk : 1, p.Hkv, p.B);
+  const dim3 cgrid(p.G + (p.max_T + kPoolChunk - 1) / kPoolChunk, p.Hkv, p.B);
   if (p.f16) decode_q4_combine_kernel<true><<<cgrid, kCombineThreads, 0, st>>>(c);
   else decode_q4_combine_kernel<false><<<cgrid, kCombineThreads, 0, st>>>(c);
   return cudaGetLastError();
 }
 
 cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st) {
-  const DecodeSplit sp = decode_split_for(p.B * p.Hkv, p.k_max, true);
+  const DecodeSplit sp = q4_split(p.B * p.Hkv, p.k_max, true);
   Q4Args a = common_args(p);
   a.tok_per_warp = sp.tok_per_warp;
   a.nsplit = sp.nsplit;
-  auto kern = p.f16 ? decode_q4_kernel<true, true> : decode_q4_kernel<true, false>;
+  auto kern = pick_kernel<true>(p.G <= 4, p.f16);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   if (sp.nsplit > 8) {

@@ -45,6 +45,7 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 
 namespace kascade {
@@ -53,14 +54,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-#ifndef Q4_MAX_TPW
-#define Q4_MAX_TPW 512
-#endif
 constexpr int kStageRows = 32;
 constexpr int kStages = 2;
+constexpr int kCtasPerSm = 3;
 constexpr uint32_t kStageBytes = kStageRows * kQ4Row;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
 constexpr uint32_t kSmemBytes = kRingBytes + 128;
+constexpr int kSlots = kCtasPerSm * 148;  // resident blocks
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kRingBytes >= kWarps * 8 * kHeadDim * sizeof(float), "the merge overlays the rings");
 
@@ -76,11 +76,11 @@ struct Q4Args {
   const int32_t* head_map;
   int k_max;
   int Hq, Hkv, G, max_T;
-  int tok_per_warp, nsplit;  // tok_per_warp is a multiple of 32
+  int B;
   float scale_log2;
   float* logits;   // anchor: [B, Hkv, max_T, G] base-2 scaled logits
-  float* part_ml;  // [B*Hkv, nsplit, G, 2]
-  float* part_o;   // [B*Hkv, nsplit, G, 128]
+  float* part_ml;  // [blocks + B*Hkv, G, 2], see Span
+  float* part_o;   // [blocks + B*Hkv, G, 128]
   uint16_t* out;   // reuse
   float* lse;
   unsigned* status;
@@ -105,6 +105,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// d = a b: a product that starts a sum (the sums' registers need no zeros first).
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -112,7 +128,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 struct Query {
   uint32_t b[4][4];   // per scale group: the two k16 steps' b0, b1
   uint32_t s0, s1;    // sum(q_g) against the minima
-  float f0, f1;       // factors of heads 2 tig, 2 tig + 1 to base-2 logits
+  float f0, f1;       // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^24)
 };
 
 template <bool PAIR, bool F16>
@@ -169,22 +185,30 @@ __device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, f
   x.f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
 }
 
-// Base-2 logits of 16 rows at shared address `rows`: s[0], s[1] are heads 2 tig, 2 tig + 1 of the
-// lane's row a, s[2], s[3] of row b = a + 8.
-__device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t row_a, int tig, float (&s)[4]) {
+// Bytes 1 and 3 of w as two half words.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
+// b - hi of half-precision subnormals (exact): the low nibbles of bytes whose high ones are hi.  On
+// the multiply-add pipe, which has more room than that of the logic operations.
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t b, uint32_t hi) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&hi));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Scores of 16 rows at shared address `rows`, in units of 2^-24: c[0], c[1] are heads 2 tig, 2 tig + 1
+// of the lane's row a, c[2], c[3] of row b = a + 8.
+__device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t row_a, int tig, float (&c)[4]) {
   const uint32_t a = rows + row_a, b = a + 8 * kQ4Row;
   const uint4 ka = lds128(a + 16 * tig), kb = lds128(b + 16 * tig);
   const uint4 ta = lds128(a + kQ4Tail), tb = lds128(b + kQ4Tail);
-  float c[4] = {0.f, 0.f, 0.f, 0.f};
   const uint32_t ma = (tig & 1) ? ta.w : ta.z, mb = (tig & 1) ? tb.w : tb.z;
-  mma_bf16_16816(c, ma, mb, ma, mb, x.s0, x.s1);
+  mma_bf16_first(c, ma, mb, ma, mb, x.s0, x.s1);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t wa = word_of(ka, g), wb = word_of(kb, g);
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_f16_16816(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, x.b[g][0], x.b[g][1]);
-    const uint32_t ha = wa >> 8, hb = wb >> 8;
-    mma_f16_16816(d, ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u, hb & 0x00f000f0u, x.b[g][2], x.b[g][3]);
+    float d[4];
+    mma_f16_first(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, x.b[g][0], x.b[g][1]);
+    const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb), ha = ua & 0x00f000f0u, hb = ub & 0x00f000f0u;
+    mma_f16_16816(d, low_nibbles(ua, ha), low_nibbles(ub, hb), ha, hb, x.b[g][2], x.b[g][3]);
     const uint32_t sa = g < 2 ? ta.x : ta.y, sb = g < 2 ? tb.x : tb.y;
     const float fa = (g & 1) ? bf16_hi(sa) : bf16_lo(sa), fb = (g & 1) ? bf16_hi(sb) : bf16_lo(sb);
     c[0] = fmaf(fa, d[0], c[0]);
@@ -192,16 +216,12 @@ __device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t r
     c[2] = fmaf(fb, d[2], c[2]);
     c[3] = fmaf(fb, d[3], c[3]);
   }
-  s[0] = c[0] * 0x1p24f * x.f0;
-  s[1] = c[1] * 0x1p24f * x.f1;
-  s[2] = c[2] * 0x1p24f * x.f0;
-  s[3] = c[3] * 0x1p24f * x.f1;
 }
 
 // Running state of a warp.  A lane's heads are 2 tig, 2 tig + 1 (PAIR: 2 (tig & 1) and the next).
 struct State {
   float m0, m1, l0, l1;
-  float o[4][2][4];  // [group][channel pair]: rows gid = channel 4 gid + 2 pair, gid + 8 = the next (times 16)
+  float o[4][2][4];  // [group][channel pair]: rows gid = channel 4 gid + 2 pair + 16 times the next, gid + 8 = the latter
   float z[4][2];     // sums of p · vm, this lane's rows
   float c[4][2];     // [group][head]: the sums o and the weights that enter them are times this power of two
 };
@@ -251,27 +271,23 @@ __device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
   return (g & 1) ? bf16_hi(w) : bf16_lo(w);
 }
 
-__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
-
 // Weights p · vs · c of this lane's rows a and b (layout of scores) as the B operands of the value
 // products, and the minima's sums.  `tail` is the address of row a's V scales.
 template <bool PAIR>
-__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], uint32_t mask, int tok_a,
+__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], bool has_a, bool has_b,
                                         uint32_t (&ba)[4], uint32_t (&bb)[4]) {
   uint4 ta = lds128(tail), tb = lds128(tail + 8 * kQ4Row);
-  if (mask != 0xffffu) {  // p is 0 there, but 0 times a stray NaN is not
-    if (!((mask >> tok_a) & 1u)) ta = make_uint4(0, 0, 0, 0);
-    if (!((mask >> (tok_a + 8)) & 1u)) tb = make_uint4(0, 0, 0, 0);
-  }
-  __half2 top = as_half2(0);
+  if (!has_a) ta = make_uint4(0, 0, 0, 0);  // p is 0 there, but 0 times a stray NaN is not
+  if (!has_b) tb = make_uint4(0, 0, 0, 0);
+  uint32_t top = 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
     ba[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
     bb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
-    top = __hmax2(top, __hmax2(as_half2(ba[g]), as_half2(bb[g])));
+    top = __vimax3_u16x2(top, ba[g], bb[g]);  // halves that are not negative compare as integers
   }
-  if (__any_sync(0xffffffffu, __hmax(__low2half(top), __high2half(top)) >= __ushort_as_half(0x7800))) {
+  if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7800u || top >= 0x78000000u)) {
     // A weight has reached 2^15: factors that put the largest weight of such a head and group in
     // [2^7, 2^8).  A weight that is not finite spoils its own sums and moves no factor.
 #pragma unroll
@@ -311,80 +327,164 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // half g % 2 of both rows' words
+    // whole bytes, and their high nibbles: the merge takes the difference of the two sums
     uint32_t x = __byte_perm(g < 2 ? e0.x : e0.y, g < 2 ? e1.x : e1.y, sel);
     uint32_t y = __byte_perm(g < 2 ? e2.x : e2.y, g < 2 ? e3.x : e3.y, sel);
-    mma_f16_16816(w.o[g][0], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ba[g], bb[g]);
-    x >>= 8;
-    y >>= 8;
-    mma_f16_16816(w.o[g][1], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, ba[g], bb[g]);
+    mma_f16_16816(w.o[g][0], x & 0x00ff00ffu, x & 0x00f000f0u, y & 0x00ff00ffu, y & 0x00f000f0u, ba[g], bb[g]);
+    x = upper_bytes(x);
+    y = upper_bytes(y);
+    mma_f16_16816(w.o[g][1], x, x & 0x00f000f0u, y, y & 0x00f000f0u, ba[g], bb[g]);
   }
+}
+
+// The anchor's work is the stages (32 tokens) of all (sequence, key head) units, one after the other,
+// and each block takes an equal share of them: the lengths are known on the device alone, and a
+// batch of one long and many short sequences then keeps every SM busy to the end.  Starting and
+// merging a unit costs a block about as much as kUnitCost stages, so a unit is that much longer on
+// the line.  A block's part of unit u goes to slot block + u of the partial results: both only ever
+// grow along the line, so no two parts meet, and the combine kernel finds a unit's slots by arithmetic.
+#ifndef Q4_UNIT_COST
+#define Q4_UNIT_COST 12
+#endif
+constexpr int kUnitCost = Q4_UNIT_COST;
+__device__ __forceinline__ int stages_of(int T, int max_T) {
+  return T > 0 && T <= max_T ? (T + kStageRows - 1) / kStageRows : 0;
+}
+__device__ __forceinline__ int length_of(int T, int max_T) {  // on the line
+  const int n = stages_of(T, max_T);
+  return n ? n + kUnitCost : 0;
+}
+// Length of all sequences and, in `before`, of the first b, for one key head.
+__device__ __forceinline__ int64_t line_length(const int32_t* seq_len, int B, int max_T, int b, int64_t& before) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  before = 0;
+  for (int i = 0; i < B; i += 32) {
+    const int n = i + lane < B ? length_of(seq_len[i + lane], max_T) : 0;
+    total += __reduce_add_sync(0xffffffffu, (unsigned)n);
+    before += __reduce_add_sync(0xffffffffu, (unsigned)(i + lane < b ? n : 0));
+  }
+  return total;
+}
+// Blocks that take part: each has some of the line, each warp has a stage where there are enough.
+__device__ __forceinline__ int working_blocks(int64_t length, int blocks) {
+  return (int)min((int64_t)blocks, (length + kWarps - 1) / kWarps);
 }
 
 // PAIR: at most 4 query heads per key head.  They are in columns 0..3 and again in 4..7, and after
 // the scores the lanes of columns 4..7 work on the second 16 rows of a stage: exponentials, weights
 // and minima then cost half.
 template <bool GATHER, bool PAIR, bool F16>
-__global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
   __shared__ float sm_po[8][kHeadDim], sm_pm[8], sm_pl[8];  // reuse: this block's part for the cluster's merge
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
 
-  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = a.G;
-  const int64_t bh = (int64_t)b * a.Hkv + h;
 
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * kStages * kStageBytes;
   const uint32_t bar = smem_u32(&bars[warp][0]);
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 2);
     mbar_fence_init();
   }
   __syncwarp();
 
-  int T = a.seq_len[b];
-  bool ok = T >= 0 && T <= a.max_T;
-  int n_items = T;
+  int b, h, T, i_begin, i_end;
   const int32_t* sel = nullptr;
-  if (GATHER && ok) {
-    const int am = a.head_map[h];
-    ok = am >= 0 && am < a.Hkv;
+  int64_t left = 0;  // anchor: what this block still has of the line
+  int at = 0;        // and where in its unit that starts
+  if constexpr (GATHER) {
+    b = blockIdx.z;
+    h = blockIdx.y;
+    T = a.seq_len[b];
+    bool ok = T >= 0 && T <= a.max_T;
+    int n_items = 0;
     if (ok) {
-      sel = a.idx + ((int64_t)b * a.Hkv + am) * a.k_max;
-      n_items = a.idx_k[b * a.Hkv + am];
-      ok = n_items >= 0 && n_items <= a.k_max;
+      const int am = a.head_map[h];
+      ok = am >= 0 && am < a.Hkv;
+      if (ok) {
+        sel = a.idx + ((int64_t)b * a.Hkv + am) * a.k_max;
+        n_items = a.idx_k[b * a.Hkv + am];
+        ok = n_items >= 0 && n_items <= a.k_max;
+      }
     }
-    if (T == 0) n_items = 0;  // nothing to gather from an empty sequence
+    if (!ok && threadIdx.x == 0 && blockIdx.x == 0) flag_status(a.status, kStatusBadIndex);
+    if (!ok || T == 0) n_items = 0;  // nothing to gather from an empty sequence
+    // a row is shared out evenly over the cluster's warps, whatever its length
+    const int parts = (int)gridDim.x * kWarps;
+    const int per_warp = ((n_items + parts - 1) / parts + kStageRows - 1) / kStageRows * kStageRows;
+    const int64_t first = (int64_t)((int)blockIdx.x * kWarps + warp) * per_warp;
+    i_begin = (int)min(first, (int64_t)n_items);
+    i_end = (int)min(first + per_warp, (int64_t)n_items);
+  } else {
+    int64_t none;
+    const int64_t total = line_length(a.seq_len, a.B, a.max_T, 0, none) * a.Hkv;
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < a.B; i += kThreads)
+        if (a.seq_len[i] < 0 || a.seq_len[i] > a.max_T) flag_status(a.status, kStatusBadIndex);
+    const int blocks = working_blocks(total, gridDim.x);
+    if ((int)blockIdx.x >= blocks) return;
+    const int64_t lo = total * blockIdx.x / blocks;
+    left = total * (blockIdx.x + 1) / blocks - lo;
+    b = h = 0;
+    int64_t base = 0;
+    for (int i = 0; i < a.B; i += 32) {  // the sequence that holds lo
+      const int n = i + lane < a.B ? length_of(a.seq_len[i + lane], a.max_T) : 0;
+      int64_t end = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += x;
+      }
+      end = (end + base) * a.Hkv;
+      const uint32_t past = __ballot_sync(0xffffffffu, end > lo);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        const int64_t in = lo - (__shfl_sync(0xffffffffu, end, l) - (int64_t)__shfl_sync(0xffffffffu, n, l) * a.Hkv);
+        const int per = __shfl_sync(0xffffffffu, n, l);
+        b = i + l;
+        h = (int)(in / per);
+        at = (int)(in - (int64_t)h * per);
+        break;
+      }
+      base = __shfl_sync(0xffffffffu, end, 31) / a.Hkv;
+    }
   }
-  if (!ok) {
-    if (threadIdx.x == 0 && split == 0) flag_status(a.status, kStatusBadIndex);
-    n_items = 0;
+  const int tok_a = (gid & 1) ? 4 + ((gid >> 1) ^ 2) : gid >> 1;  // token of fragment row gid
+  const uint32_t row_a = (uint32_t)tok_a * kQ4Row;
+  // PAIR: this lane's rows of a stage are the first 16 or, from tig 2 on, the second
+  const uint32_t half = PAIR && tig >= 2 ? 16 : 0;
+  const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
+  int st = 0, phase = 0;
+  bool alive = true;
+
+  while (true) {
+  if constexpr (!GATHER) {
+    T = a.seq_len[b];
+    const int n = stages_of(T, a.max_T), end = (int)min((int64_t)at + left, (int64_t)(n + kUnitCost));
+    if (end <= max(at, kUnitCost)) return;  // nothing left, or no stage of the last unit
+    left -= end - at;
+    const int s0 = max(at - kUnitCost, 0), ns = end - kUnitCost - s0;
+    i_begin = (s0 + (int)((int64_t)ns * warp / kWarps)) * kStageRows;
+    i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
   }
-  // A reuse row is shared out evenly over the cluster's warps, whatever its length.
-  const int tok_per_warp =
-      GATHER ? ((n_items + a.nsplit * kWarps - 1) / (a.nsplit * kWarps) + 31) & ~31 : a.tok_per_warp;
-  if (!GATHER && (int64_t)split * kWarps * tok_per_warp >= n_items) return;  // the combine kernel skips this part
-  const int64_t first = (int64_t)(split * kWarps + warp) * tok_per_warp;
-  const int i_begin = (int)min(first, (int64_t)n_items);
-  const int i_end = (int)min(first + tok_per_warp, (int64_t)n_items);
+  const int64_t bh = (int64_t)b * a.Hkv + h;
   const int n_iter = (i_end - i_begin + kStageRows - 1) / kStageRows;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
   // Row addresses run ahead of the copies: the selected token two stages, its place in the pages one.
   auto token_of = [&](int it) -> int {
     const int i = i_begin + kStageRows * it + lane;
-    if (i >= i_end) return -1;
-    if constexpr (GATHER) {
-      const int t = __ldg(sel + i);
-      if (t < 0 || t >= T) flag_status(a.status, kStatusBadIndex);
-      return t < T ? t : -1;  // negative: skipped
-    } else {
-      return i;
-    }
+    if (!GATHER || i >= i_end) return i < i_end ? i : -1;
+    const int t = __ldg(sel + i);
+    if (t < 0 || t >= T) flag_status(a.status, kStatusBadIndex);
+    return t < T ? t : -1;  // negative: skipped
   };
   auto place_of = [&](int t) -> int {  // row of the page store, or -1
     if (t < 0) return -1;
@@ -404,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
     place_next = place_of(token_next);
     token_next = token_of(it + 2);
     mask = __ballot_sync(0xffffffffu, place >= 0);
-    const uint32_t dst = ring + (uint32_t)st * kStageBytes, br = bar + 8 * st;
+    const uint32_t dst = ring + (uint32_t)st * kStageBytes;
     if constexpr (GATHER) {
       // 320 chunks of 16 bytes, ten to a row; the two of a 32-byte sector go to neighbouring lanes
 #pragma unroll
@@ -414,13 +514,12 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
         cp_async16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
                    pl >= 0 ? 16 : 0);
       }
-    } else {
-      if (lane == 0) mbar_expect_tx(br, (uint32_t)__popc(mask) * kQ4Row);
-      __syncwarp();
-      // 16 tokens that start at a multiple of 16 lie in one page, one behind the other
-      const uint32_t rows = (uint32_t)__popc((lane < 16 ? mask : mask >> 16) & 0xffffu);
-      if ((lane & 15) == 0 && rows)
-        bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, rows * kQ4Row, br);
+    } else if ((lane & 15) == 0) {
+      // 16 tokens that start at a multiple of 16 lie in one page, one behind the other: two copies,
+      // each announced by its own lane (of no bytes, where the rows are past the end or the page is bad)
+      const uint32_t bytes = (uint32_t)__popc((mask >> lane) & 0xffffu) * kQ4Row;
+      mbar_expect_tx(bar + 8 * st, bytes);
+      if (bytes) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, bytes, bar + 8 * st);
     }
   };
 
@@ -436,21 +535,16 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
   }
-  const int tok_a = (gid & 1) ? 4 + ((gid >> 1) ^ 2) : gid >> 1;  // token of fragment row gid
-  const uint32_t row_a = (uint32_t)tok_a * kQ4Row;
-  float* lrow = a.logits + bh * a.max_T * G;
-
-  // PAIR: this lane's rows of a stage are the first 16 or, from tig 2 on, the second
-  const uint32_t half = PAIR && tig >= 2 ? 16 : 0;
-  const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
+  float* lrow = a.logits + (bh * a.max_T + i_begin + (int)half + tok_a) * G + col;
+  const bool two_heads = !(G & 1) && col < G;  // one aligned store of both
+  float base0 = 0.f, base1 = 0.f;              // finite_max of the maxima
 
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (s < n_iter) issue(s, s, masks[s]);
+    if (s < n_iter) issue(s, (st + s) % kStages, masks[s]);
     if constexpr (GATHER) cp_async_commit();
   }
-  int st = 0, phase = 0, st_in = kStages - 1;
-  bool alive = true;
+  int st_in = (st + kStages - 1) % kStages;
   int it = 0;
   for (; it < n_iter; ++it) {
     if (it + kStages - 1 < n_iter) issue(it + kStages - 1, st_in, masks[kStages - 1]);
@@ -473,27 +567,34 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[0][i] = half ? s[1][i] : s[0][i];
     }
-    if (mask != 0xffffffffu) {
 #pragma unroll
-      for (int u = 0; u < kSets; ++u) {
-        if (!((mask >> (16 * u + half + tok_a)) & 1u)) s[u][0] = s[u][1] = -INFINITY;
-        if (!((mask >> (16 * u + half + tok_a + 8)) & 1u)) s[u][2] = s[u][3] = -INFINITY;
+    for (int u = 0; u < kSets; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p24f * ((i & 1) ? qx.f1 : qx.f0);
+    const bool full = mask == 0xffffffffu;
+    bool has[4] = {true, true, true, true};  // the lane's rows: a and b of each set
+    if (!full) {
+#pragma unroll
+      for (int u = 0; u < 2 * kSets; ++u) {
+        has[u] = (mask >> (8 * u + half + tok_a)) & 1u;
+        if (!has[u]) s[u >> 1][2 * (u & 1)] = s[u >> 1][2 * (u & 1) + 1] = -INFINITY;
       }
     }
     if constexpr (!GATHER) {
-      const int t0 = i_begin + kStageRows * it + (int)half + tok_a;
+      const int rest = i_end - (i_begin + kStageRows * it + (int)half + tok_a);
 #pragma unroll
       for (int u = 0; u < 2 * kSets; ++u) {
-        const int t = t0 + 8 * u;
+        float* p = lrow + 8 * u * G;
         const float x0 = s[u >> 1][2 * (u & 1)], x1 = s[u >> 1][2 * (u & 1) + 1];
-        if (t < i_end) {
-          if (!(G & 1) && col < G) *reinterpret_cast<float2*>(lrow + (int64_t)t * G + col) = make_float2(x0, x1);
-          else if (col < G) {
-            lrow[(int64_t)t * G + col] = x0;
-            if (col + 1 < G) lrow[(int64_t)t * G + col + 1] = x1;
+        if (full || rest > 8 * u) {
+          if (two_heads) *reinterpret_cast<float2*>(p) = make_float2(x0, x1);
+          else {
+            if (col < G) p[0] = x0;
+            if (col + 1 < G) p[1] = x1;
           }
         }
       }
+      lrow += kStageRows * G;
     }
     float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
     if constexpr (!PAIR) {
@@ -502,7 +603,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
     }
     if (__any_sync(0xffffffffu, x0 > w.m0 + 8.f || x1 > w.m1 + 8.f)) {
       const float n0 = fmaxf(w.m0, head_max<PAIR>(x0)), n1 = fmaxf(w.m1, head_max<PAIR>(x1));
-      const float al0 = fast_exp2(w.m0 - finite_max(n0)), al1 = fast_exp2(w.m1 - finite_max(n1));
+      base0 = finite_max(n0);
+      base1 = finite_max(n1);
+      const float al0 = fast_exp2(w.m0 - base0), al1 = fast_exp2(w.m1 - base1);
       w.m0 = n0;
       w.m1 = n1;
       w.l0 *= al0;
@@ -510,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
       rebase(w, 0, al0);
       rebase(w, 1, al1);
     }
-    const float base0 = finite_max(w.m0), base1 = finite_max(w.m1);
     uint32_t ba[4], bb[4];
 #pragma unroll
     for (int u = 0; u < kSets; ++u) {
@@ -518,8 +620,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
       for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
       w.l0 += s[u][0] + s[u][2];
       w.l1 += s[u][1] + s[u][3];
-      weights<PAIR>(w, rows + (16 * u + half) * kQ4Row + row_a + kQ4Tail + 16, s[u], (mask >> (16 * u + half)) & 0xffffu,
-                    tok_a, ba, bb);
+      weights<PAIR>(w, rows + (16 * u + half) * kQ4Row + row_a + kQ4Tail + 16, s[u], has[2 * u], has[2 * u + 1], ba, bb);
       values(w, rows + 16 * u * kQ4Row, gid, tig, ba, bb);
     }
     if constexpr (PAIR) {
@@ -562,8 +663,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
   }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^24 / c, every second
-                                                                        // channel in 1/16 of that
+    const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^-24 c
     const float z0 = head_sum<PAIR>(w.z[g][0]), z1 = head_sum<PAIR>(w.z[g][1]);
     if (!owner) continue;
 #pragma unroll
@@ -571,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
       const int d = 32 * g + 4 * gid + 2 * u;
       const float* o = w.o[g][u];
       *reinterpret_cast<float2*>(&sm_o[warp][col][d]) =
-          make_float2(fmaf(o[0] * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
+          make_float2(fmaf((o[0] - o[2]) * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
       *reinterpret_cast<float2*>(&sm_o[warp][col + 1][d]) =
-          make_float2(fmaf(o[1] * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
+          make_float2(fmaf((o[1] - o[3]) * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
     }
   }
   __syncthreads();
@@ -595,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
         sm_pl[g] = L;
       }
     } else {
-      const int64_t slot = (bh * a.nsplit + split) * G + g;
+      const int64_t slot = ((int64_t)blockIdx.x + bh) * G + g;
       a.part_o[slot * kHeadDim + d] = acc;
       if (d == 0) {
         a.part_ml[slot * 2] = M;
@@ -623,12 +723,24 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q4_kernel(const Q4Args a) 
       }
     }
     cluster.sync();  // peers keep their shared memory until rank 0 has read it
+    return;
+  }
+  // the next unit; a warp that gave up takes its whole block along
+  fence_proxy_async_smem();  // the merge wrote where the next copies go
+  if (__syncthreads_or(!alive) || left <= 0) return;
+  at = 0;
+  if (++h == a.Hkv) {
+    h = 0;
+    do ++b;
+    while (b < a.B && stages_of(a.seq_len[b], a.max_T) == 0);
+    if (b == a.B) return;
+  }
   }
 }
 
 struct CombineArgs {
   const int32_t* seq_len;
-  int Hq, Hkv, G, max_T, nsplit, per_split;  // per_split: tokens of a split
+  int B, Hq, Hkv, G, max_T, blocks;  // blocks: grid of the first kernel
   const float* part_ml;
   const float* part_o;
   const float* logits;
@@ -657,8 +769,17 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   const bool merge = blockIdx.x < G;
   const int chunk = (int)blockIdx.x - G;
   if (!merge && (int64_t)chunk * kPoolChunk >= T) return;
-  const int ns = (T + a.per_split - 1) / a.per_split;  // splits that hold tokens
-  const float* ml = a.part_ml + bh * a.nsplit * G * 2;
+  // the slots of this unit: those of the blocks that hold its first stage to its last
+  int64_t before;
+  const int64_t total = line_length(a.seq_len, a.B, a.max_T, b, before) * a.Hkv;
+  const int mine = length_of(T, a.max_T), blocks = working_blocks(total, a.blocks);
+  int c0 = 0, ns = 0;
+  if (mine) {
+    const int64_t first = before * a.Hkv + (int64_t)h * mine;  // block c starts at total c / blocks
+    c0 = (int)(((first + kUnitCost + 1) * blocks - 1) / total);
+    ns = (int)(((first + mine) * blocks - 1) / total) - c0 + 1;
+  }
+  const float* ml = a.part_ml + (c0 + bh) * G * 2;
   if (merge ? warp == 0 : warp < G) {
     const int g = merge ? (int)blockIdx.x : warp;
     float M = -INFINITY, L = 0.f;
@@ -677,7 +798,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   __syncthreads();
   if (merge) {
     const int g = (int)blockIdx.x;
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + bh * a.nsplit * G * kHeadDim) + g * 32 + lane;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + (c0 + bh) * G * kHeadDim) + g * 32 + lane;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = warp; s < ns; s += kCombineThreads / 32) {
@@ -722,34 +843,33 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   }
 }
 
+// Blocks of the anchor's first kernel: one wave, or fewer where the warps would have no stage.
+int anchor_blocks(int64_t units, int max_T) {
+  const int64_t stages = units * ((max_T + kStageRows - 1) / kStageRows + kUnitCost);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kSlots, (stages + kWarps - 1) / kWarps));
+}
+
+// Blocks (one cluster) per reuse row: one wave, at least a stage per warp.
+int reuse_split(int64_t units, int k_max) {
+  const int64_t n = std::min<int64_t>(std::min<int64_t>(16, std::max<int64_t>(1, kSlots / units)),
+                                      ((int64_t)k_max + kWarps * kStageRows - 1) / (kWarps * kStageRows));
+  return (int)std::max<int64_t>(1, n);
+}
+
 struct WsLayout {
   size_t logits, part_ml, part_o, total;
 };
-WsLayout ws_layout(int B, int Hkv, int G, int max_T, int nsplit) {
+WsLayout ws_layout(int B, int Hkv, int G, int max_T) {
   WsLayout w;
+  const size_t slots = (size_t)B * Hkv + anchor_blocks((int64_t)B * Hkv, max_T);
   size_t off = 0;
   w.logits = off;
   off = align_up(off + (size_t)B * Hkv * max_T * G * sizeof(float), 256);
   w.part_ml = off;
-  off = align_up(off + (size_t)B * Hkv * nsplit * G * 2 * sizeof(float), 256);
+  off = align_up(off + slots * G * 2 * sizeof(float), 256);
   w.part_o = off;
-  w.total = align_up(off + (size_t)B * Hkv * nsplit * G * kHeadDim * sizeof(float), 256);
+  w.total = align_up(off + slots * G * kHeadDim * sizeof(float), 256);
   return w;
-}
-
-// Work split of `units` (sequence, key head) rows of up to n_items tokens.
-DecodeSplit q4_split(int units, int n_items, bool gather) {
-  constexpr int kSlots = 4 * 148;  // resident blocks
-  DecodeSplit s;
-  int64_t nsplit = units >= kSlots ? 1 : kSlots / units;  // one wave
-  if (gather && nsplit > 16) nsplit = 16;                 // the splits of a row are one cluster
-  const int64_t per = kWarps * nsplit;
-  int64_t tpw = ((n_items + per - 1) / per + 31) / 32 * 32;
-  if (tpw < 32) tpw = 32;
-  if (!gather && tpw > Q4_MAX_TPW) tpw = Q4_MAX_TPW;
-  s.tok_per_warp = (int)tpw;
-  s.nsplit = n_items > 0 ? (int)((n_items + kWarps * tpw - 1) / (kWarps * tpw)) : 1;
-  return s;
 }
 
 Q4Args common_args(const DecodeQ4Params& p) {
@@ -761,7 +881,7 @@ Q4Args common_args(const DecodeQ4Params& p) {
   while (((int64_t)2 << a.page_shift) < p.page_size) ++a.page_shift;
   a.page_mul = (uint32_t)(((uint64_t)1 << (32 + a.page_shift)) / (uint64_t)p.page_size + 1);
   a.seq_len = p.seq_len; a.idx = p.idx; a.idx_k = p.idx_k; a.head_map = p.head_map; a.k_max = p.k_max;
-  a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G; a.max_T = p.max_T;
+  a.B = p.B; a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G; a.max_T = p.max_T;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.out = p.out; a.lse = p.lse; a.status = p.status;
   return a;
@@ -776,29 +896,25 @@ auto pick_kernel(bool pair, bool f16) {
 }  // namespace
 
 size_t decode_q4_workspace_bytes(int B, int Hkv, int G, int max_T) {
-  return ws_layout(B, Hkv, G, max_T, q4_split(B * Hkv, max_T, false).nsplit).total;
+  return ws_layout(B, Hkv, G, max_T).total;
 }
 
 cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
-  const DecodeSplit sp = q4_split(p.B * p.Hkv, p.max_T, false);
-  const WsLayout w = ws_layout(p.B, p.Hkv, p.G, p.max_T, sp.nsplit);
+  const int blocks = anchor_blocks((int64_t)p.B * p.Hkv, p.max_T);
+  const WsLayout w = ws_layout(p.B, p.Hkv, p.G, p.max_T);
   char* ws = static_cast<char*>(p.ws);
   Q4Args a = common_args(p);
-  a.tok_per_warp = sp.tok_per_warp;
-  a.nsplit = sp.nsplit;
   a.logits = reinterpret_cast<float*>(ws + w.logits);
   a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
-  const dim3 grid(sp.nsplit, p.Hkv, p.B);
   auto kern = pick_kernel<false>(p.G <= 4, p.f16);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, kSmemBytes, st>>>(a);
+  kern<<<blocks, kThreads, kSmemBytes, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   CombineArgs c;
   c.seq_len = p.seq_len;
-  c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.nsplit = sp.nsplit;
-  c.per_split = kWarps * sp.tok_per_warp;
+  c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.B = p.B; c.blocks = blocks;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
   const dim3 cgrid(p.G + (p.max_T + kPoolChunk - 1) / kPoolChunk, p.Hkv, p.B);
@@ -808,25 +924,23 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
 }
 
 cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st) {
-  const DecodeSplit sp = q4_split(p.B * p.Hkv, p.k_max, true);
+  const int nsplit = reuse_split((int64_t)p.B * p.Hkv, p.k_max);
   Q4Args a = common_args(p);
-  a.tok_per_warp = sp.tok_per_warp;
-  a.nsplit = sp.nsplit;
   auto kern = pick_kernel<true>(p.G <= 4, p.f16);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  if (sp.nsplit > 8) {
+  if (nsplit > 8) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sp.nsplit, p.Hkv, p.B);
+  cfg.gridDim = dim3(nsplit, p.Hkv, p.B);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = sp.nsplit;
+  attr[0].val.clusterDim.x = nsplit;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;

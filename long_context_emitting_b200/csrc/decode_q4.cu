@@ -55,12 +55,16 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageRows = 32;
-constexpr int kStages = 2;
+#ifndef Q4_STAGES
+#define Q4_STAGES 2
+#endif
+constexpr int kStages = Q4_STAGES;
 constexpr int kCtasPerSm = 3;
 constexpr uint32_t kStageBytes = kStageRows * kQ4Row;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
 constexpr uint32_t kSmemBytes = kRingBytes + 128;
 constexpr int kSlots = kCtasPerSm * 148;  // resident blocks
+constexpr int kNoToken = -2147483647 - 1;  // lanes past the end
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kRingBytes >= kWarps * 8 * kHeadDim * sizeof(float), "the merge overlays the rings");
 
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   const uint32_t half = PAIR && tig >= 2 ? 16 : 0;
   const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
   int st = 0, phase = 0;
-  bool alive = true;
+  bool alive = true, bad = false;  // bad: an index or page out of range was met
 
   while (true) {
   if constexpr (!GATHER) {
@@ -478,31 +482,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   const int n_iter = (i_end - i_begin + kStageRows - 1) / kStageRows;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
-  // Row addresses run ahead of the copies: the selected token two stages, its place in the pages one.
-  auto token_of = [&](int it) -> int {
+  // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
+  // and neither is looked at before the next stage's turn.
+  auto load_token = [&](int it) -> int {
     const int i = i_begin + kStageRows * it + lane;
-    if (!GATHER || i >= i_end) return i < i_end ? i : -1;
-    const int t = __ldg(sel + i);
-    if (t < 0 || t >= T) flag_status(a.status, kStatusBadIndex);
-    return t < T ? t : -1;  // negative: skipped
+    if (i >= i_end) return kNoToken;
+    return GATHER ? __ldg(sel + i) : i;
   };
-  auto place_of = [&](int t) -> int {  // row of the page store, or -1
-    if (t < 0) return -1;
-    const int pi = (int)(__umulhi((uint32_t)t, a.page_mul) >> a.page_shift);
-    const int page = __ldg(table + pi);
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-      flag_status(a.status, kStatusBadIndex);
-      return -1;
+  int token_2 = load_token(0), token_1 = kNoToken, page_1 = 0, page_index = 0;
+  auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
+    token_1 = token_2;
+    if (GATHER && (token_1 < 0 || token_1 >= T)) {
+      bad |= i_begin + kStageRows * it + lane < i_end;
+      token_1 = kNoToken;
     }
-    return (page * a.Hkv + h) * a.page_size + (t - pi * a.page_size);
+    if (token_1 != kNoToken) {
+      page_index = (int)(__umulhi((uint32_t)token_1, a.page_mul) >> a.page_shift);
+      page_1 = __ldg(table + page_index);
+    }
+    token_2 = load_token(it + 1);
   };
-  int token_next = token_of(1);
-  int place_next = place_of(token_of(0));
+  load_page(0);
   uint32_t masks[kStages];  // rows present, stage by stage in order of use
   auto issue = [&](int it, int st, uint32_t& mask) {
-    const int place = place_next;
-    place_next = place_of(token_next);
-    token_next = token_of(it + 2);
+    int place = -1;  // row of the page store
+    if (token_1 != kNoToken) {
+      place = (page_1 * a.Hkv + h) * a.page_size + (token_1 - page_index * a.page_size);
+      if ((unsigned)page_1 >= (unsigned)a.num_pages) {
+        bad = true;
+        place = -1;
+      }
+    }
+    load_page(it + 1);
     mask = __ballot_sync(0xffffffffu, place >= 0);
     const uint32_t dst = ring + (uint32_t)st * kStageBytes;
     if constexpr (GATHER) {
@@ -649,6 +660,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       mbar_wait(bar + 8 * st, (uint32_t)phase, a.status);
     }
   }
+
+  if (bad) flag_status(a.status, kStatusBadIndex);
+  bad = false;
 
   // ---- merge the four warps; the rings are free once all are here ------------
   const float l0 = head_sum<PAIR>(w.l0), l1 = head_sum<PAIR>(w.l1);

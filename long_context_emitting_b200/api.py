@@ -7,6 +7,7 @@ runs in the library's kernels; CPU tensors are rejected.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
@@ -58,13 +59,16 @@ _DATA_DTYPES = (torch.bfloat16, torch.float16)
 def _data_suffix(*ts) -> str:
     """'' for bfloat16 q/k/v/out, '_f16' for float16 (all of one call alike)."""
     dt = ts[0].dtype
-    if dt not in _DATA_DTYPES or any(t.dtype != dt for t in ts):
+    same = dt in _DATA_DTYPES
+    for t in ts:
+        same = same and t.dtype == dt
+    if not same:
         raise TypeError("q, k, v must all be bfloat16 or all float16")
     return "_f16" if dt == torch.float16 else ""
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def k_for_len(n: int) -> int:
@@ -241,17 +245,23 @@ def _need_rows(name: str, t, dtype: torch.dtype, shape: tuple) -> None:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.stride(-1) != 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
 
 
 def _need_one_device(t0: torch.Tensor, **others) -> None:
-    dev = t0.device
+    dev = t0.get_device()
     for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {t0.device}")
+
+
+# A decode step makes some of these calls for every layer: what a call does not have to build anew
+# on the host (structures of its sizes, by value) is not.
+_shape = functools.lru_cache(maxsize=256)(Shape)
+_strides = functools.lru_cache(maxsize=1024)(Strides)
 
 
 def _call(dev: torch.device, name: str, *args) -> None:
@@ -267,23 +277,28 @@ def _call(dev: torch.device, name: str, *args) -> None:
 
 
 def _span(t: torch.Tensor):
-    """First byte of a view and the byte after its last."""
+    """First byte of a [., ., ., 128] view of 16-bit rows and the byte after its last."""
     a = t.data_ptr()
-    return a, a + (sum((n - 1) * st for n, st in zip(t.shape, t.stride())) + 1) * t.element_size()
+    (n0, n1, n2, n3), (s0, s1, s2, s3) = t.shape, t.stride()
+    return a, a + 2 * ((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + (n3 - 1) * s3 + 1)
 
 
-def _need_apart(name: str, out: torch.Tensor, ins) -> None:
-    """An output is one of its inputs exactly, or shares no memory with any."""
-    if out.numel() == 0:
-        return
-    a, b = _span(out)
-    for t in ins:
-        if t.data_ptr() == a and t.stride() == out.stride() and t.shape == out.shape:
-            return
-    for t in ins:
-        lo, hi = _span(t)
-        if lo < b and a < hi:
-            raise ValueError(f"{name} overlaps an input without being the same view")
+def _need_apart(ins, outs) -> None:
+    """Each output [B, H, N, 128] is one of the inputs [B, N, H, 128] exactly, or
+    shares no memory with any."""
+    spans = [_span(t) for t in ins]
+    for name, out in outs:
+        a, b = _span(out)
+        overlaps = False
+        for t, (lo, hi) in zip(ins, spans):
+            if lo < b and a < hi:
+                t = t.transpose(1, 2)
+                if lo == a and t.stride() == out.stride() and t.shape == out.shape:
+                    break
+                overlaps = True
+        else:
+            if overlaps:
+                raise ValueError(f"{name} overlaps an input without being the same view")
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -317,13 +332,13 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     _need_rows("k_out", k_out, q.dtype, (B, Hkv, N, d))
     _need_one_device(q, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight,
                      q_out=q_out, k_out=k_out)
-    _need_apart("q_out", q_out, (q.transpose(1, 2), k.transpose(1, 2)))
-    _need_apart("k_out", k_out, (k.transpose(1, 2), q.transpose(1, 2)))
-    _call(q.device, "kascade_qk_norm_rope" + sfx, Shape(B, Hq, Hkv, d), N,
-          _ptr(q), Strides(*q.stride()[:3]), _ptr(k), Strides(*k.stride()[:3]), _ptr(positions), _ptr(inv_freq),
+    if B and N:
+        _need_apart((q, k), (("q_out", q_out), ("k_out", k_out)))
+    _call(q.device, "kascade_qk_norm_rope" + sfx, _shape(B, Hq, Hkv, d), N,
+          _ptr(q), _strides(*q.stride()[:3]), _ptr(k), _strides(*k.stride()[:3]), _ptr(positions), _ptr(inv_freq),
           _ptr(q_weight), _ptr(k_weight), float(eps), int(bool(interleaved)),
-          _ptr(q_out), Strides(q_out.stride(0), q_out.stride(2), q_out.stride(1)),
-          _ptr(k_out), Strides(k_out.stride(0), k_out.stride(2), k_out.stride(1)))
+          _ptr(q_out), _strides(q_out.stride(0), q_out.stride(2), q_out.stride(1)),
+          _ptr(k_out), _strides(k_out.stride(0), k_out.stride(2), k_out.stride(1)))
     return q_out, k_out
 
 
@@ -357,9 +372,9 @@ def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=
     if count is not None:
         _need_size("count", count, torch.int32, B)
     _need_one_device(k, v=v, kv_pages=kv_pages, block_table=block_table, start=start, count=count)
-    _call(k.device, "kascade_kv_write_paged_q4" + sfx, Shape(B, Hkv, Hkv, d), N,
-          _ptr(k), Strides(k.stride(0), k.stride(2), k.stride(1)),
-          _ptr(v), Strides(v.stride(0), v.stride(2), v.stride(1)), _ptr(kv_pages), kv_pages.shape[0],
+    _call(k.device, "kascade_kv_write_paged_q4" + sfx, _shape(B, Hkv, Hkv, d), N,
+          _ptr(k), _strides(k.stride(0), k.stride(2), k.stride(1)),
+          _ptr(v), _strides(v.stride(0), v.stride(2), v.stride(1)), _ptr(kv_pages), kv_pages.shape[0],
           _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count))
     return kv_pages
 
@@ -383,7 +398,7 @@ def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int
     for name, t in (("k", k), ("v", v)):
         _need_size(name, t, dtype, B * Hkv * N * HEAD_DIM)
     _need_one_device(kv_pages, block_table=block_table, start=start, count=count, k=k, v=v)
-    _call(kv_pages.device, "kascade_kv_read_paged_q4" + sfx, Shape(B, Hkv, Hkv, HEAD_DIM), int(N), _ptr(kv_pages),
+    _call(kv_pages.device, "kascade_kv_read_paged_q4" + sfx, _shape(B, Hkv, Hkv, HEAD_DIM), int(N), _ptr(kv_pages),
           kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count),
           _ptr(k), _ptr(v))
     return k, v
@@ -411,7 +426,7 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     _need_size("out", out, q.dtype, B * Hq * d)
     _need_size("lse", lse, torch.float32, B * Hq)
     _need_size("pooled", pooled, torch.float32, B * Hkv * ld_pooled)
-    shape = Shape(B, Hq, Hkv, d)
+    shape = _shape(B, Hq, Hkv, d)
     if ws is None:
         ws = workspace(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T), dev)
     _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, out=out, lse=lse,
@@ -442,7 +457,7 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     _need_size("lse", lse, torch.float32, B * Hq)
     _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, idx=idx, idx_k=idx_k,
                      head_map=head_map, out=out, lse=lse)
-    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, Shape(B, Hq, Hkv, d), _ptr(q), _ptr(kv_pages),
+    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, _shape(B, Hq, Hkv, d), _ptr(q), _ptr(kv_pages),
           kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(seq_len), _ptr(idx),
           _ptr(idx_k), int(k_max), _ptr(head_map), float(scale), _ptr(out), _ptr(lse))
     return out, lse

@@ -769,10 +769,12 @@ constexpr int kPoolChunk = 1024;  // tokens per block
 
 // Second kernel of the anchor.  Blocks x < G merge the outputs of one head over the splits, eight
 // splits at a time; the others turn a chunk of logits into pooled probabilities.  Each works out the
-// maxima and sums that it needs from the splits'.
-template <bool F16>
+// maxima and sums that it needs from the splits'; a chunk's logits are loaded before that.  V: float4
+// per token of the logits (G = 4 V), 0 for other G.
+template <bool F16, int V>
 __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(const CombineArgs a) {
-  __shared__ float s_M[8], s_L[8], s_lse2[8];
+  __shared__ float s_M[8], s_L[8];
+  __shared__ __align__(16) float s_lse2[8];
   __shared__ float4 s_o[kCombineThreads / 32][kHeadDim / 4];
   const int b = blockIdx.z, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -783,6 +785,18 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   const bool merge = blockIdx.x < G;
   const int chunk = (int)blockIdx.x - G;
   if (!merge && (int64_t)chunk * kPoolChunk >= T) return;
+  const float* lrow = a.logits + bh * a.max_T * G;
+  constexpr int kPer = kPoolChunk / kCombineThreads;  // tokens per thread
+  float4 x[V > 0 ? kPer : 1][V > 0 ? V : 1];
+  if (V > 0 && !merge) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = chunk * kPoolChunk + i * kCombineThreads + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        x[i][j] = t < T ? reinterpret_cast<const float4*>(lrow)[(int64_t)t * V + j] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
   // the slots of this unit: those of the blocks that hold its first stage to its last
   int64_t before;
   const int64_t total = line_length(a.seq_len, a.B, a.max_T, b, before) * a.Hkv;
@@ -806,7 +820,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
     if (lane == 0) {
       s_M[g] = finite_max(M);
       s_L[g] = L;
-      s_lse2[g] = lse2_of(M, L);
+      s_lse2[g] = merge ? lse2_of(M, L) : finite_max(lse2_of(M, L));
     }
   }
   __syncthreads();
@@ -834,26 +848,29 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
     if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = s_lse2[g] * kLn2;
     return;
   }
-  const int t_hi = (int)min((int64_t)(chunk + 1) * kPoolChunk, (int64_t)T);
-  const float* lrow = a.logits + bh * a.max_T * G;
   float* prow = a.pooled + bh * a.ld_pooled;
   const float invG = 1.f / (float)G;
   // no finite score at all (every page entry bad): relative to 0 the probabilities are 0
-  if (G == 4) {
-    float x[4];
+  if constexpr (V > 0) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) x[g] = finite_max(s_lse2[g]);
-#pragma unroll 4
-    for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
-      const float4 v = reinterpret_cast<const float4*>(lrow)[t];
-      prow[t] = 0.25f * (fast_exp2(v.x - x[0]) + fast_exp2(v.y - x[1]) + fast_exp2(v.z - x[2]) + fast_exp2(v.w - x[3]));
+    for (int i = 0; i < kPer; ++i) {
+      const int t = chunk * kPoolChunk + i * kCombineThreads + threadIdx.x;
+      float acc = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float4 l = *reinterpret_cast<const float4*>(&s_lse2[4 * j]);
+        acc += (fast_exp2(x[i][j].x - l.x) + fast_exp2(x[i][j].y - l.y)) +
+               (fast_exp2(x[i][j].z - l.z) + fast_exp2(x[i][j].w - l.w));
+      }
+      if (t < T) prow[t] = acc * invG;
     }
-    return;
-  }
-  for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
-    float acc = 0.f;
-    for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - finite_max(s_lse2[g]));
-    prow[t] = acc * invG;
+  } else {
+    const int t_hi = (int)min((int64_t)(chunk + 1) * kPoolChunk, (int64_t)T);
+    for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
+      float acc = 0.f;
+      for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - s_lse2[g]);
+      prow[t] = acc * invG;
+    }
   }
 }
 
@@ -901,6 +918,12 @@ Q4Args common_args(const DecodeQ4Params& p) {
   return a;
 }
 
+auto pick_combine(int G, bool f16) {
+  if (G == 4) return f16 ? decode_q4_combine_kernel<true, 1> : decode_q4_combine_kernel<false, 1>;
+  if (G == 8) return f16 ? decode_q4_combine_kernel<true, 2> : decode_q4_combine_kernel<false, 2>;
+  return f16 ? decode_q4_combine_kernel<true, 0> : decode_q4_combine_kernel<false, 0>;
+}
+
 template <bool GATHER>
 auto pick_kernel(bool pair, bool f16) {
   return pair ? (f16 ? decode_q4_kernel<GATHER, true, true> : decode_q4_kernel<GATHER, true, false>)
@@ -932,8 +955,8 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
   const dim3 cgrid(p.G + (p.max_T + kPoolChunk - 1) / kPoolChunk, p.Hkv, p.B);
-  if (p.f16) decode_q4_combine_kernel<true><<<cgrid, kCombineThreads, 0, st>>>(c);
-  else decode_q4_combine_kernel<false><<<cgrid, kCombineThreads, 0, st>>>(c);
+  auto comb = pick_combine(p.G, p.f16);
+  comb<<<cgrid, kCombineThreads, 0, st>>>(c);
   return cudaGetLastError();
 }
 

@@ -40,6 +40,9 @@ struct RopeArgs {
   int heads_per_block;
 };
 
+// An output may be its input's own view, so these are ordinary loads, not read-only ones.
+__device__ __forceinline__ uint4 load_row(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
 // TOK tokens x kRows / TOK heads at a time.
 template <int TOK, bool F16, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
@@ -58,63 +61,78 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   __syncthreads();
 
   const int row = threadIdx.x / 8, j = threadIdx.x % 8;
-  const int t = row % TOK, n = n0 + t;
-  const int h_end = min(a.H, (int)(blockIdx.y + 1) * a.heads_per_block);
-  for (int hh = blockIdx.y * a.heads_per_block; hh < h_end; hh += kRows / TOK) {
-    // a warp's four rows may lie past the end: they compute on the last row and store nothing
-    const int h = min(hh + row / TOK, h_end - 1);
-    const bool live = hh + row / TOK < h_end && n < a.N;
-    const int part = h >= a.Hq;
-    const int hp = part ? h - a.Hq : h;
-    const kascade_strides& xs = a.xs[part];
-    const uint16_t* x = a.x[part] + (int64_t)b * xs.b + (int64_t)min(n, a.N - 1) * xs.n + (int64_t)hp * xs.h + 8 * j;
-    const uint4 c0 = ldg16(x), c1 = ldg16(x + 64);
-    float v[16];
+  const int t = row % TOK, n = min(n0 + t, a.N - 1);
+  const int h_lo = blockIdx.y * a.heads_per_block, h_hi = min(a.H, h_lo + a.heads_per_block);
+  constexpr int kStep = kRows / TOK;
+  // The query heads of the block, then its key heads; the next rows are on their way while some are
+  // worked on.  Rows past the end compute on the last one and store nothing.
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      unpack2<F16>(word_of(c0, i), v[2 * i], v[2 * i + 1]);
-      unpack2<F16>(word_of(c1, i), v[8 + 2 * i], v[8 + 2 * i + 1]);
+  for (int part = 0; part < 2; ++part) {
+    const int first = part ? max(h_lo, a.Hq) - a.Hq : h_lo, end = part ? h_hi - a.Hq : min(h_hi, a.Hq);
+    if (first >= end) continue;
+    const kascade_strides &xs = a.xs[part], &ys = a.ys[part];
+    const uint16_t* x = a.x[part] + (int64_t)b * xs.b + (int64_t)n * xs.n + 8 * j;
+    uint16_t* y = a.y[part] + (int64_t)b * ys.b + (int64_t)n * ys.n + 8 * j;
+    const bool norm = a.w[part] != nullptr;
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (norm) {
+      w0 = ldg16(a.w[part] + 8 * j);
+      w1 = ldg16(a.w[part] + 64 + 8 * j);
     }
-    if (a.w[part]) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) ss += v[i] * v[i];
-      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-      ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-      const float r = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-      const uint4 w0 = ldg16(a.w[part] + 8 * j), w1 = ldg16(a.w[part] + 64 + 8 * j);
+    int h = first + row / TOK;
+    const uint16_t* x0 = x + (int64_t)min(h, end - 1) * xs.h;
+    uint4 c0 = load_row(x0), c1 = load_row(x0 + 64);
+    for (int hh = first; hh < end; hh += kStep, h += kStep) {
+      float v[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        unpack2<F16>(word_of(w0, i), lo, hi);
-        v[2 * i] *= r * lo;
-        v[2 * i + 1] *= r * hi;
-        unpack2<F16>(word_of(w1, i), lo, hi);
-        v[8 + 2 * i] *= r * lo;
-        v[8 + 2 * i + 1] *= r * hi;
+        unpack2<F16>(word_of(c0, i), v[2 * i], v[2 * i + 1]);
+        unpack2<F16>(word_of(c1, i), v[8 + 2 * i], v[8 + 2 * i + 1]);
       }
-    }
-    float o[16];
+      if (hh + kStep < end) {
+        const uint16_t* x1 = x + (int64_t)min(h + kStep, end - 1) * xs.h;
+        c0 = load_row(x1);
+        c1 = load_row(x1 + 64);
+      }
+      if (norm) {
+        float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (INTER) {  // pairs (2i, 2i+1) of chunk 0, then of chunk 1
-        const float2 r = cs[t][i < 4 ? 4 * j + i : 32 + 4 * j + i - 4];
-        o[2 * i] = v[2 * i] * r.x - v[2 * i + 1] * r.y;
-        o[2 * i + 1] = v[2 * i + 1] * r.x + v[2 * i] * r.y;
-      } else {                // channel 8j + i with 64 + 8j + i
-        const float2 r = cs[t][8 * j + i];
-        o[i] = v[i] * r.x - v[8 + i] * r.y;
-        o[8 + i] = v[8 + i] * r.x + v[i] * r.y;
+        for (int i = 0; i < 16; ++i) ss += v[i] * v[i];
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+        const float r = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          unpack2<F16>(word_of(w0, i), lo, hi);
+          v[2 * i] *= r * lo;
+          v[2 * i + 1] *= r * hi;
+          unpack2<F16>(word_of(w1, i), lo, hi);
+          v[8 + 2 * i] *= r * lo;
+          v[8 + 2 * i + 1] *= r * hi;
+        }
       }
-    }
-    if (live) {
-      const kascade_strides& ys = a.ys[part];
-      uint16_t* y = a.y[part] + (int64_t)b * ys.b + (int64_t)n * ys.n + (int64_t)hp * ys.h + 8 * j;
-      *reinterpret_cast<uint4*>(y) = make_uint4(pack_x2<F16>(o[0], o[1]), pack_x2<F16>(o[2], o[3]),
-                                                pack_x2<F16>(o[4], o[5]), pack_x2<F16>(o[6], o[7]));
-      *reinterpret_cast<uint4*>(y + 64) = make_uint4(pack_x2<F16>(o[8], o[9]), pack_x2<F16>(o[10], o[11]),
-                                                     pack_x2<F16>(o[12], o[13]), pack_x2<F16>(o[14], o[15]));
+      float o[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (INTER) {  // pairs (2i, 2i+1) of chunk 0, then of chunk 1
+          const float2 r = cs[t][i < 4 ? 4 * j + i : 32 + 4 * j + i - 4];
+          o[2 * i] = v[2 * i] * r.x - v[2 * i + 1] * r.y;
+          o[2 * i + 1] = v[2 * i + 1] * r.x + v[2 * i] * r.y;
+        } else {                // channel 8j + i with 64 + 8j + i
+          const float2 r = cs[t][8 * j + i];
+          o[i] = v[i] * r.x - v[8 + i] * r.y;
+          o[8 + i] = v[8 + i] * r.x + v[i] * r.y;
+        }
+      }
+      if (h < end && n0 + t < a.N) {
+        uint16_t* d = y + (int64_t)h * ys.h;
+        *reinterpret_cast<uint4*>(d) = make_uint4(pack_x2<F16>(o[0], o[1]), pack_x2<F16>(o[2], o[3]),
+                                                  pack_x2<F16>(o[4], o[5]), pack_x2<F16>(o[6], o[7]));
+        *reinterpret_cast<uint4*>(d + 64) = make_uint4(pack_x2<F16>(o[8], o[9]), pack_x2<F16>(o[10], o[11]),
+                                                       pack_x2<F16>(o[12], o[13]), pack_x2<F16>(o[14], o[15]));
+      }
     }
   }
 }

@@ -8,14 +8,13 @@
 //   s = the smallest bfloat16 >= (max(x) - m) / 15      (so no value clips)
 //   n = (x - m) / s rounded to nearest, half to even, in 0..15 (0 when s = 0)
 //   value = m + s n
-// m and s are rounded outward with the directed roundings of fp32 and one
-// truncation, which is exact because every bfloat16 bound is also an fp32
-// number.  n comes from one multiplication by 1 / s, off by less than 2^-17, and
-// is certain unless the quotient lies within 2^-16 of a half-way point (or s is
-// so small that 1 / s is not a normal number).  Those lanes divide: fp32 division
-// is monotone and cannot round a quotient that is not half-way onto a half-way
-// point; only the subtraction x - m may, when it is inexact, and then its
-// rounding error (two-sum) says to which side the value lies.
+// m and s are rounded outward.  s is a product with a little less than 1/15,
+// rounded up to bfloat16 and moved up once more if 15 s is still below the
+// range: 15 s is an fp32 number, so that is decided exactly.  n comes from a
+// product with an approximate 1 / s.  Its remainder r = (x - m) - n s is exact
+// in fp32, and where r is not clearly below s / 2 the code is settled by r and,
+// where x - m was inexact, by its rounding error (two-sum).  Half-way points are
+// common (a 16-bit value on an 8-bit grid), so that path is short too.
 //
 // What bounds both kernels: memory, 512 bytes of 16-bit rows against 160 bytes
 // of cache row per token and key head.  Half a warp handles one row: a lane
@@ -63,96 +62,88 @@ __device__ __forceinline__ uint32_t bf16_up_pos(float x) {  // x >= 0
   return ((u & 0xffffu) ? u + 0x10000u : u) >> 16;
 }
 
-struct Group {
-  uint32_t words;  // 8 codes of this lane
-  uint32_t s, m;   // bfloat16 bits of the group's scale and minimum
-  bool bad;        // a value is not finite, or the range is not
-};
-
-// Minima (or maxima) of the halves of two words, in the data's type; a NaN loses.
+// Minima of the halves of two words, in the data's type; a NaN stays.
 template <bool F16>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   if constexpr (F16) {
-    const __half2 r = __hmin2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
     const __nv_bfloat162 r =
-        __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
   }
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-  return min2<F16>(a ^ 0x80008000u, b ^ 0x80008000u) ^ 0x80008000u;
+constexpr uint32_t kSigns = 0x80008000u;
+
+__device__ __forceinline__ float approx_rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The code of x by division, for values next to a half-way point.
-__device__ __noinline__ uint32_t exact_code(float x, float m, float s) {
-  const float d = __fadd_rn(x, -m);
-  const float q = __fdiv_rn(d, s);
-  float n = rintf(q);
-  const float f = floorf(q);
-  if (q - f == 0.5f) {  // half-way: the rounding error of d, if any, decides
-    const float bb = __fadd_rn(d, -x);
-    const float err = __fadd_rn(__fadd_rn(x, -__fadd_rn(d, -bb)), __fadd_rn(-m, -bb));
-    if (err > 0.f) n = f + 1.f;
-    if (err < 0.f) n = f;
-  }
-  return (uint32_t)(int)fminf(fmaxf(n, 0.f), 15.f);
+// Minimum and minus maximum of the group's values, packed in the data's type.
+template <bool F16>
+__device__ __forceinline__ uint32_t group_ends(const uint4& w) {
+  const uint32_t lo = min2<F16>(min2<F16>(w.x, w.y), min2<F16>(w.z, w.w));
+  const uint32_t hi = min2<F16>(min2<F16>(w.x ^ kSigns, w.y ^ kSigns), min2<F16>(w.z ^ kSigns, w.w ^ kSigns));
+  uint32_t ends = min2<F16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+  ends = min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+  return min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+}
+
+struct Scale {
+  float s, m, inv;
+  bool bad;  // a value is not finite, or the range is not
+};
+template <bool F16>
+__device__ __forceinline__ Scale group_scale(uint32_t ends) {
+  float lo, hi;
+  unpack2<F16>(ends, lo, hi);
+  Scale g;
+  g.m = __uint_as_float(bf16_down(lo) << 16);
+  const float range = __fadd_ru(-hi, -g.m);
+  uint32_t s = bf16_up_pos(range * 0x1.11110cp-4f);  // 1/15 less 2^-22 of it
+  if (fmaf(__uint_as_float(s << 16), 15.f, -range) < 0.f) ++s;
+  g.s = __uint_as_float(s << 16);
+  g.inv = approx_rcp(fmaxf(g.s, 0x1p-120f));
+  g.bad = !(range < CUDART_INF_F);
+  return g;
 }
 
 // Codes of this lane's 8 values; lanes 4g .. 4g+3 of the half warp are one group.
 template <bool F16>
-__device__ __forceinline__ Group quantise(const uint4& w) {
-  float x[8];
-  float none = 0.f;  // NaN as soon as a value is not finite
+__device__ __forceinline__ uint32_t codes(const uint4& w, float s, float m, float inv) {
+  float x[8], n[8], r[8];
+  float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    unpack2<F16>(word_of(w, i), x[2 * i], x[2 * i + 1]);
-    none = fmaf(x[2 * i], 0.f, fmaf(x[2 * i + 1], 0.f, none));
-  }
-  const uint32_t lo2 = min2<F16>(min2<F16>(w.x, w.y), min2<F16>(w.z, w.w));
-  const uint32_t hi2 = max2<F16>(max2<F16>(w.x, w.y), max2<F16>(w.z, w.w)) ^ 0x80008000u;
-  // (minimum, minus maximum) in one word
-  uint32_t ends = min2<F16>(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
-  ends = min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
-  ends = min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
-  float lo, hi;
-  unpack2<F16>(ends, lo, hi);
-  hi = -hi;
-  const uint32_t odd = __ballot_sync(0xffffffffu, !(none == 0.f));
-  Group g;
-  g.m = bf16_down(lo);
-  const float m = __uint_as_float(g.m << 16);
-  g.s = bf16_up_pos(__fdiv_ru(__fadd_ru(hi, -m), 15.f));
-  const float s = __uint_as_float(g.s << 16);
-  g.bad = ((odd >> (threadIdx.x & 28)) & 15u) || !(s < CUDART_INF_F && fabsf(m) < CUDART_INF_F);
-  g.words = 0;
-  if (g.bad) {  // reads back as NaN: the loss shows
-    g.s = 0;
-    g.m = 0x7fc0u;
-    return g;
-  }
-  if (s == 0.f) return g;
-  const float inv = __frcp_rn(s);
-  float near = s < 0x1p-100f ? 1.f : 0.f;  // distance to the code, at most 1/2
-  float n[8];
+  for (int i = 0; i < 4; ++i) unpack2<F16>(word_of(w, i), x[2 * i], x[2 * i + 1]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float d = x[i] - m;
     n[i] = fmaf(d, inv, 0x1.8p23f) - 0x1.8p23f;  // rounds to an integer
-    near = fmaxf(near, fabsf(fmaf(d, inv, -n[i])));
+    r[i] = fmaf(-n[i], s, d);
+    most = fmaxf(most, fabsf(r[i]));
+  }
+  if (most >= s * (0.5f - 0x1p-15f) && s > 0.f) {  // without a range all codes are 0
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s < 0x1p-120f) {  // 1 / s is out of range: start from a quotient of scaled numbers
+        n[i] = rintf(((x[i] - m) * 0x1p64f) / (s * 0x1p64f));
+        r[i] = fmaf(-n[i], s, x[i] - m);
+      }
+      const float d = x[i] - m, back = d - x[i];
+      const float lost = (x[i] - (d - back)) + (-m - back);  // x - m is d + lost
+      const float over = fmaf(2.f, r[i], -s) + 2.f * lost, under = fmaf(2.f, r[i], s) + 2.f * lost;
+      const bool odd = (int)n[i] & 1;
+      if (over > 0.f || (over == 0.f && odd)) n[i] += 1.f;
+      if (under < 0.f || (under == 0.f && odd)) n[i] -= 1.f;
+    }
   }
   // four codes in 16 bits: exact in fp32, and read off the low bits after adding 2^23
   const float a = fmaf(n[3], 4096.f, fmaf(n[2], 256.f, fmaf(n[1], 16.f, n[0]))) + 0x1p23f;
   const float b = fmaf(n[7], 4096.f, fmaf(n[6], 256.f, fmaf(n[5], 16.f, n[4]))) + 0x1p23f;
-  g.words = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
-  if (near > 0.5f - 0x1p-16f) {
-    g.words = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g.words |= exact_code(x[i], m, s) << (4 * i);
-  }
-  return g;
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
 // Where a half warp works: one token of a tile of TOK, through heads h, h + kRows / TOK, ... < h_end.
@@ -217,20 +208,28 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
       nk = ldg16(k);
       nv = ldg16(v);
     }
-    const Group gk = quantise<F16>(ck), gv = quantise<F16>(cv);
+    // even lanes work out K's scale of their group, odd lanes V's
+    const uint32_t ek = group_ends<F16>(ck), ev = group_ends<F16>(cv);
+    Scale mine = group_scale<F16>((l & 1) ? ev : ek);
+    const uint32_t bits = mine.bad ? 0x7fc00000u : (__float_as_uint(mine.m) | (__float_as_uint(mine.s) >> 16));
+    const int lk = threadIdx.x & 30, lv = lk + 1;
+    const uint32_t tk = __shfl_sync(0xffffffffu, bits, lk), tv = __shfl_sync(0xffffffffu, bits, lv);
+    const float ik = __shfl_sync(0xffffffffu, mine.inv, lk), iv = __shfl_sync(0xffffffffu, mine.inv, lv);
+    // a group that is not finite reads back as NaN: scale 0, minimum NaN (its codes are any)
+    const uint32_t kwords = codes<F16>(ck, bf16_lo(tk), bf16_hi(tk), ik);
+    const uint32_t vwords = codes<F16>(cv, bf16_lo(tv), bf16_hi(tv), iv);
     // lane (g, j) holds channels 32g + 8j ..: V half words of lane groups r = 2j and 2j + 1.  Even g
     // builds the word of r = 2j (halves g, g + 1), odd g that of r = 2j + 1.
-    const uint32_t give = odd ? gv.words & 0xffffu : gv.words >> 16;
+    const uint32_t give = odd ? vwords & 0xffffu : vwords >> 16;
     const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
-    const uint32_t vword = odd ? (got | (gv.words & 0xffff0000u)) : ((gv.words & 0xffffu) | (got << 16));
+    const uint32_t vword = odd ? (got | (vwords & 0xffff0000u)) : ((vwords & 0xffffu) | (got << 16));
     // bfloat16 number l of the tail: K scales, K minima, V scales, V minima, by groups
     const int src = (threadIdx.x & 16) + 4 * (l & 3);
-    const uint32_t tk = __shfl_sync(0xffffffffu, gk.s | (gk.m << 16), src);
-    const uint32_t tv = __shfl_sync(0xffffffffu, gv.s | (gv.m << 16), src);
-    const uint32_t tw = l < 8 ? tk : tv;
+    const uint32_t wk = __shfl_sync(0xffffffffu, tk, src), wv = __shfl_sync(0xffffffffu, tv, src);
+    const uint32_t tw = l < 8 ? wk : wv;
     if (live) {
-      bad |= gk.bad || gv.bad;
-      reinterpret_cast<uint32_t*>(dst)[4 * j + g] = gk.words;
+      bad |= mine.bad;
+      reinterpret_cast<uint32_t*>(dst)[4 * j + g] = kwords;
       reinterpret_cast<uint32_t*>(dst + kQ4V)[2 * (2 * j + (int)odd) + (g >> 1)] = vword;
       reinterpret_cast<uint16_t*>(dst + kQ4Tail)[l] = (uint16_t)((l & 4) ? tw >> 16 : tw);
     }

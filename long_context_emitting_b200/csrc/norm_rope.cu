@@ -64,6 +64,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   const int t = row % TOK, n = min(n0 + t, a.N - 1);
   const int h_lo = blockIdx.y * a.heads_per_block, h_hi = min(a.H, h_lo + a.heads_per_block);
   constexpr int kStep = kRows / TOK;
+  float2 turn[8];  // this lane's pairs
+#pragma unroll
+  for (int i = 0; i < 8; ++i) turn[i] = cs[t][!INTER ? 8 * j + i : i < 4 ? 4 * j + i : 32 + 4 * j + i - 4];
   // The query heads of the block, then its key heads; the next rows are on their way while some are
   // worked on.  Rows past the end compute on the last one and store nothing.
 #pragma unroll
@@ -117,11 +120,11 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if constexpr (INTER) {  // pairs (2i, 2i+1) of chunk 0, then of chunk 1
-          const float2 r = cs[t][i < 4 ? 4 * j + i : 32 + 4 * j + i - 4];
+          const float2 r = turn[i];
           o[2 * i] = v[2 * i] * r.x - v[2 * i + 1] * r.y;
           o[2 * i + 1] = v[2 * i + 1] * r.x + v[2 * i] * r.y;
         } else {                // channel 8j + i with 64 + 8j + i
-          const float2 r = cs[t][8 * j + i];
+          const float2 r = turn[i];
           o[i] = v[i] * r.x - v[8 + i] * r.y;
           o[8 + i] = v[8 + i] * r.x + v[i] * r.y;
         }

@@ -182,6 +182,7 @@ struct Place {
 
 template <int TOK, bool F16>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a) {
+  overlap_launches();
   const Place<TOK> p(a);
   // whole warps leave together: a tile past the end of its sequence costs nothing more
   if (!__any_sync(0xffffffffu, p.row >= 0)) return;
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
 
 template <int TOK, bool F16>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a) {
+  overlap_launches();
   const Place<TOK> p(a);
   if (!__any_sync(0xffffffffu, p.row >= 0)) return;
   const int l = threadIdx.x % 16;
@@ -299,8 +301,7 @@ cudaError_t launch_tok(CacheArgs& a, int B, bool f16, bool write, cudaStream_t s
   const dim3 grid((unsigned)blocks, (a.Hkv + a.heads_per_block - 1) / a.heads_per_block);
   auto kern = write ? (f16 ? cache_write_kernel<TOK, true> : cache_write_kernel<TOK, false>)
                     : (f16 ? cache_read_kernel<TOK, true> : cache_read_kernel<TOK, false>);
-  kern<<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, grid, kThreads, 0, st, a);
 }
 
 }  // namespace

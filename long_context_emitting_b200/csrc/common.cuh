@@ -32,6 +32,29 @@ __device__ __forceinline__ void allow_dependents_launch() {
 }
 
 // The launch attribute of programmatic dependent launch.
+inline cudaLaunchAttribute pdl_attribute();
+
+// Launch of a kernel that starts with overlap_launches(): its blocks may take their places while the
+// stream's previous kernel drains, and the next such kernel's while this one does.
+template <typename... K, typename... A>
+cudaError_t launch_overlapped(void (*kern)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+// First statement of such a kernel, in every thread: nothing is read or written before the previous
+// kernel's effects are there, and so none completes before those in front of it.
+__device__ __forceinline__ void overlap_launches() {
+  allow_dependents_launch();
+  grid_dependency_wait();
+}
+
 inline cudaLaunchAttribute pdl_attribute() {
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

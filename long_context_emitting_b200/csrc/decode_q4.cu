@@ -380,6 +380,7 @@ __device__ __forceinline__ int working_blocks(int64_t length, int blocks) {
 // and minima then cost half.
 template <bool GATHER, bool PAIR, bool F16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q4Args a) {
+  overlap_launches();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
@@ -407,17 +408,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     b = blockIdx.z;
     h = blockIdx.y;
     T = a.seq_len[b];
-    bool ok = T >= 0 && T <= a.max_T;
-    int n_items = 0;
-    if (ok) {
-      const int am = a.head_map[h];
-      ok = am >= 0 && am < a.Hkv;
-      if (ok) {
-        sel = a.idx + ((int64_t)b * a.Hkv + am) * a.k_max;
-        n_items = a.idx_k[b * a.Hkv + am];
-        ok = n_items >= 0 && n_items <= a.k_max;
-      }
-    }
+    const int am = a.head_map[h], row = b * a.Hkv + min(max(am, 0), a.Hkv - 1);
+    int n_items = a.idx_k[row];
+    const bool ok = T >= 0 && T <= a.max_T && am >= 0 && am < a.Hkv && n_items >= 0 && n_items <= a.k_max;
+    sel = a.idx + (int64_t)row * a.k_max;
     if (!ok && threadIdx.x == 0 && blockIdx.x == 0) flag_status(a.status, kStatusBadIndex);
     if (!ok || T == 0) n_items = 0;  // nothing to gather from an empty sequence
     // a row is shared out evenly over the cluster's warps, whatever its length
@@ -489,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     if (i >= i_end) return kNoToken;
     return GATHER ? __ldg(sel + i) : i;
   };
-  int token_2 = load_token(0), token_1 = kNoToken, page_1 = 0, page_index = 0;
+  const int token_0 = load_token(0);  // on its way, as is the first page of the anchor, while q is
+  int token_2 = token_0, token_1 = kNoToken, page_1 = 0, page_index = 0;
   auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
     token_1 = token_2;
     if (GATHER && (token_1 < 0 || token_1 >= T)) {
@@ -502,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
     token_2 = load_token(it + 1);
   };
-  load_page(0);
+  if (!GATHER) load_page(0);
   uint32_t masks[kStages];  // rows present, stage by stage in order of use
   auto issue = [&](int it, int st, uint32_t& mask) {
     int place = -1;  // row of the page store
@@ -536,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 
   Query qx;
   load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
+  if (GATHER) load_page(0);
   State w;
   w.m0 = w.m1 = -INFINITY;
   w.l0 = w.l1 = 0.f;
@@ -773,6 +769,7 @@ constexpr int kPoolChunk = 1024;  // tokens per block
 // per token of the logits (G = 4 V), 0 for other G.
 template <bool F16, int V>
 __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(const CombineArgs a) {
+  overlap_launches();
   __shared__ float s_M[8], s_L[8];
   __shared__ __align__(16) float s_lse2[8];
   __shared__ float4 s_o[kCombineThreads / 32][kHeadDim / 4];
@@ -947,17 +944,15 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   auto kern = pick_kernel<false>(p.G <= 4, p.f16);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<blocks, kThreads, kSmemBytes, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_overlapped(kern, blocks, kThreads, kSmemBytes, st, a);
+  if (e != cudaSuccess) return e;
   CombineArgs c;
   c.seq_len = p.seq_len;
   c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.B = p.B; c.blocks = blocks;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
   const dim3 cgrid(p.G + (p.max_T + kPoolChunk - 1) / kPoolChunk, p.Hkv, p.B);
-  auto comb = pick_combine(p.G, p.f16);
-  comb<<<cgrid, kCombineThreads, 0, st>>>(c);
-  return cudaGetLastError();
+  return launch_overlapped(pick_combine(p.G, p.f16), cgrid, kCombineThreads, 0, st, c);
 }
 
 cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st) {
@@ -975,13 +970,14 @@ cudaError_t launch_decode_reuse_q4(const DecodeQ4Params& p, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1] = pdl_attribute();
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = nsplit;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -46,6 +46,7 @@ __device__ __forceinline__ uint4 load_row(const uint16_t* p) { return *reinterpr
 // TOK tokens x kRows / TOK heads at a time.
 template <int TOK, bool F16, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
+  overlap_launches();
   __shared__ float2 cs[TOK][kHeadDim / 2];
   const int b = blockIdx.x / a.tiles;
   const int n0 = (blockIdx.x - b * a.tiles) * TOK;
@@ -153,8 +154,7 @@ cudaError_t launch_tok(RopeArgs& a, int B, bool f16, bool interleaved, cudaStrea
   const dim3 grid((unsigned)blocks, (a.H + a.heads_per_block - 1) / a.heads_per_block);
   auto kern = f16 ? (interleaved ? qk_norm_rope_kernel<TOK, true, true> : qk_norm_rope_kernel<TOK, true, false>)
                   : (interleaved ? qk_norm_rope_kernel<TOK, false, true> : qk_norm_rope_kernel<TOK, false, false>);
-  kern<<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, grid, kThreads, 0, st, a);
 }
 
 }  // namespace

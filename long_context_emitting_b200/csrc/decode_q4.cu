@@ -55,10 +55,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageRows = 32;
-#ifndef Q4_STAGES
-#define Q4_STAGES 2
-#endif
-constexpr int kStages = Q4_STAGES;
+constexpr int kStages = 2;
 constexpr int kCtasPerSm = 3;
 constexpr uint32_t kStageBytes = kStageRows * kQ4Row;
 constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
@@ -102,6 +99,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+
 // Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -128,15 +131,19 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// The query operand: heads are the 8 columns, head gid of a lane's fragments.
+// The query operand: heads are the 8 columns, head gid of a lane's fragments.  With PAIR there are
+// two of them, for the first and the second 16 rows of a stage: the heads in columns 0..3 and zeros
+// in the others, and zeros there and the heads in columns 4..7.  Both products go to one sum, which
+// then holds the scores of 32 rows.
+template <bool PAIR>
 struct Query {
-  uint32_t b[4][4];   // per scale group: the two k16 steps' b0, b1
-  uint32_t s0, s1;    // sum(q_g) against the minima
-  float f0, f1;       // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^24)
+  uint32_t b[PAIR ? 2 : 1][4][4];  // per scale group: the two k16 steps' b0, b1
+  uint32_t s[PAIR ? 2 : 1][2];     // sum(q_g) against the minima
+  float f0, f1;                    // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^24)
 };
 
 template <bool PAIR, bool F16>
-__device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, float scale_log2, int gid, int tig) {
+__device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, int G, float scale_log2, int gid, int tig) {
   float v[4][8];
   float top = 0.f;
 #pragma unroll
@@ -171,10 +178,10 @@ __device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, f
     sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
     sum[g] *= 0x1p-24f;  // the codes' unit
     // code j of a word is in half j / 4; odd j carry 16 times their code
-    x.b[g][0] = pack_f16x2(v[g][0], v[g][4]);
-    x.b[g][1] = pack_f16x2(v[g][1] * 0.0625f, v[g][5] * 0.0625f);
-    x.b[g][2] = pack_f16x2(v[g][2], v[g][6]);
-    x.b[g][3] = pack_f16x2(v[g][3] * 0.0625f, v[g][7] * 0.0625f);
+    x.b[0][g][0] = pack_f16x2(v[g][0], v[g][4]);
+    x.b[0][g][1] = pack_f16x2(v[g][1] * 0.0625f, v[g][5] * 0.0625f);
+    x.b[0][g][2] = pack_f16x2(v[g][2], v[g][6]);
+    x.b[0][g][3] = pack_f16x2(v[g][3] * 0.0625f, v[g][7] * 0.0625f);
   }
   // k = 0..3: leading term of sum_g against minimum g, 4..7: second, 8..11: third, 12..15: nothing
   const float u0 = (tig & 1) ? sum[2] : sum[0], u1 = (tig & 1) ? sum[3] : sum[1];
@@ -182,8 +189,23 @@ __device__ __forceinline__ void load_query(Query& x, const uint16_t* q, int G, f
   const float r0 = u0 - bf16_lo(hi), r1 = u1 - bf16_hi(hi);
   const uint32_t mid = pack_bf16x2(r0, r1);
   const uint32_t lo = pack_bf16x2(r0 - bf16_lo(mid), r1 - bf16_hi(mid));
-  x.s0 = tig < 2 ? hi : mid;
-  x.s1 = tig < 2 ? lo : 0u;
+  x.s[0][0] = tig < 2 ? hi : mid;
+  x.s[0][1] = tig < 2 ? lo : 0u;
+  if constexpr (PAIR) {
+    const uint32_t m = gid < 4 ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t& q0 = x.b[0][i >> 2][i & 3];
+      q0 &= m;
+      // lanes gid and gid ^ 4 change places (a mask instead would be applied anew in every stage)
+      x.b[1][i >> 2][i & 3] = __shfl_xor_sync(0xffffffffu, q0, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x.s[0][i] &= m;
+      x.s[1][i] = __shfl_xor_sync(0xffffffffu, x.s[0][i], 16);
+    }
+  }
   const float f = scale_log2 * pow2i(e);
   x.f0 = __shfl_sync(0xffffffffu, f, 8 * tig);
   x.f1 = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
@@ -198,23 +220,44 @@ __device__ __forceinline__ uint32_t low_nibbles(uint32_t b, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// Scores of 16 rows at shared address `rows`, in units of 2^-24: c[0], c[1] are heads 2 tig, 2 tig + 1
-// of the lane's row a, c[2], c[3] of row b = a + 8.
-__device__ __forceinline__ void scores(const Query& x, uint32_t rows, uint32_t row_a, int tig, float (&c)[4]) {
-  const uint32_t a = rows + row_a, b = a + 8 * kQ4Row;
-  const uint4 ka = lds128(a + 16 * tig), kb = lds128(b + 16 * tig);
-  const uint4 ta = lds128(a + kQ4Tail), tb = lds128(b + kQ4Tail);
-  const uint32_t ma = (tig & 1) ? ta.w : ta.z, mb = (tig & 1) ? tb.w : tb.z;
-  mma_bf16_first(c, ma, mb, ma, mb, x.s0, x.s1);
+// Products of the codes in words wa and wb (of a lane's rows a and b) with the query.
+template <bool FIRST>
+__device__ __forceinline__ void score_codes(float (&d)[4], uint32_t wa, uint32_t wb, const uint32_t (&q)[4]) {
+  const uint32_t la = wa & 0x000f000fu, lb = wb & 0x000f000fu, ga = wa & 0x00f000f0u, gb = wb & 0x00f000f0u;
+  if constexpr (FIRST) mma_f16_first(d, la, lb, ga, gb, q[0], q[1]);
+  else mma_f16_16816(d, la, lb, ga, gb, q[0], q[1]);
+  const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb), ha = ua & 0x00f000f0u, hb = ub & 0x00f000f0u;
+  mma_f16_16816(d, low_nibbles(ua, ha), low_nibbles(ub, hb), ha, hb, q[2], q[3]);
+}
+
+// Scores of SETS x 16 rows at shared address `rows`, in units of 2^-24: c[0], c[1] are the lane's two
+// heads of its row a, c[2], c[3] of row b = a + 8.  `mine` is the address of the lane's own row a.
+template <bool PAIR>
+__device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint32_t row_a, uint32_t mine, int tig,
+                                       uint32_t mask, int tok_a, float (&c)[4]) {
+  constexpr int kSets = PAIR ? 2 : 1;
+  const uint2 sa = lds64(mine + kQ4Tail), sb = lds64(mine + 8 * kQ4Row + kQ4Tail);
+  uint4 ka[kSets], kb[kSets];
+#pragma unroll
+  for (int u = 0; u < kSets; ++u) {
+    const uint32_t a = rows + 16 * u * kQ4Row + row_a, b = a + 8 * kQ4Row;
+    ka[u] = lds128(a + 16 * tig);
+    kb[u] = lds128(b + 16 * tig);
+    uint32_t ma = lds32(a + kQ4Tail + 8 + 4 * (tig & 1)), mb = lds32(b + kQ4Tail + 8 + 4 * (tig & 1));
+    if (PAIR && mask != 0xffffffffu) {  // what is left of older rows times the zeros of a column may be NaN
+      if (!((mask >> (16 * u + tok_a)) & 1u)) ma = 0;
+      if (!((mask >> (16 * u + tok_a + 8)) & 1u)) mb = 0;
+    }
+    if (u == 0) mma_bf16_first(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
+    else mma_bf16_16816(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
+  }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const uint32_t wa = word_of(ka, g), wb = word_of(kb, g);
     float d[4];
-    mma_f16_first(d, wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u, x.b[g][0], x.b[g][1]);
-    const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb), ha = ua & 0x00f000f0u, hb = ub & 0x00f000f0u;
-    mma_f16_16816(d, low_nibbles(ua, ha), low_nibbles(ub, hb), ha, hb, x.b[g][2], x.b[g][3]);
-    const uint32_t sa = g < 2 ? ta.x : ta.y, sb = g < 2 ? tb.x : tb.y;
-    const float fa = (g & 1) ? bf16_hi(sa) : bf16_lo(sa), fb = (g & 1) ? bf16_hi(sb) : bf16_lo(sb);
+    score_codes<true>(d, word_of(ka[0], g), word_of(kb[0], g), x.b[0][g]);
+    if constexpr (PAIR) score_codes<false>(d, word_of(ka[1], g), word_of(kb[1], g), x.b[1][g]);
+    const uint32_t wa = g < 2 ? sa.x : sa.y, wb = g < 2 ? sb.x : sb.y;
+    const float fa = (g & 1) ? bf16_hi(wa) : bf16_lo(wa), fb = (g & 1) ? bf16_hi(wb) : bf16_lo(wb);
     c[0] = fmaf(fa, d[0], c[0]);
     c[1] = fmaf(fa, d[1], c[1]);
     c[2] = fmaf(fb, d[2], c[2]);
@@ -380,14 +423,17 @@ __device__ __forceinline__ int working_blocks(int64_t length, int blocks) {
 // and minima then cost half.
 template <bool GATHER, bool PAIR, bool F16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q4Args a) {
-  overlap_launches();
+  // (clusters of the next reuse call, were they let in early, would leave some SMs to fewer of its blocks)
+  if (!GATHER) allow_dependents_launch();
+  grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][8], sm_l[kWarps][8];
   __shared__ float sm_po[8][kHeadDim], sm_pm[8], sm_pl[8];  // reuse: this block's part for the cluster's merge
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // known to be the same in all lanes
+  const int lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = a.G;
 
@@ -529,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
   };
 
-  Query qx;
+  Query<PAIR> qx;
   load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
   if (GATHER) load_page(0);
   State w;
@@ -567,13 +613,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     const uint32_t rows = ring + (uint32_t)st * kStageBytes;
     const uint32_t mask = masks[0];
     constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
-    float s[2][4];
-    scores(qx, rows, row_a, tig, s[0]);
-    scores(qx, rows + 16 * kQ4Row, row_a, tig, s[1]);
-    if constexpr (PAIR) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[0][i] = half ? s[1][i] : s[0][i];
-    }
+    const uint32_t mine = rows + half * kQ4Row + row_a;
+    float s[kSets][4];
+    scores<PAIR>(qx, rows, row_a, mine, tig, mask, tok_a, s[0]);
+    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1]);
 #pragma unroll
     for (int u = 0; u < kSets; ++u)
 #pragma unroll
@@ -627,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
       w.l0 += s[u][0] + s[u][2];
       w.l1 += s[u][1] + s[u][3];
-      weights<PAIR>(w, rows + (16 * u + half) * kQ4Row + row_a + kQ4Tail + 16, s[u], has[2 * u], has[2 * u + 1], ba, bb);
+      weights<PAIR>(w, mine + 16 * u * kQ4Row + kQ4Tail + 16, s[u], has[2 * u], has[2 * u + 1], ba, bb);
       values(w, rows + 16 * u * kQ4Row, gid, tig, ba, bb);
     }
     if constexpr (PAIR) {

@@ -106,10 +106,17 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 }
 
 // Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) that completes on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// Read once: these lines leave L2 first, so that the logits find room there until they are pooled.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 // d = a b: a product that starts a sum (the sums' registers need no zeros first).
@@ -505,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   // PAIR: this lane's rows of a stage are the first 16 or, from tig 2 on, the second
   const uint32_t half = PAIR && tig >= 2 ? 16 : 0;
   const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
+  const uint64_t policy = read_once_policy();
   int st = 0, phase = 0;
   bool alive = true, bad = false;  // bad: an index or page out of range was met
 
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       // each announced by its own lane (of no bytes, where the rows are past the end or the page is bad)
       const uint32_t bytes = (uint32_t)__popc((mask >> lane) & 0xffffu) * kQ4Row;
       mbar_expect_tx(bar + 8 * st, bytes);
-      if (bytes) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, bytes, bar + 8 * st);
+      if (bytes) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, bytes, bar + 8 * st, policy);
     }
   };
 
@@ -793,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 
 struct CombineArgs {
   const int32_t* seq_len;
-  int B, Hq, Hkv, G, max_T, blocks;  // blocks: grid of the first kernel
+  int B, Hq, Hkv, G, max_T, blocks, chunk;  // blocks: grid of the first kernel
   const float* part_ml;
   const float* part_o;
   const float* logits;
@@ -804,7 +812,7 @@ struct CombineArgs {
 };
 
 constexpr int kCombineThreads = 256;
-constexpr int kPoolChunk = 1024;  // tokens per block
+constexpr int kPoolBatch = 1024;  // tokens of a block in flight; a block has some batches (chunk tokens)
 
 // Second kernel of the anchor.  Blocks x < G merge the outputs of one head over the splits, eight
 // splits at a time; the others turn a chunk of logits into pooled probabilities.  Each works out the
@@ -823,20 +831,23 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   int T = a.seq_len[b];
   if (T < 0 || T > a.max_T) T = 0;
   const bool merge = blockIdx.x < G;
-  const int chunk = (int)blockIdx.x - G;
-  if (!merge && (int64_t)chunk * kPoolChunk >= T) return;
+  const int64_t t_lo = merge ? 0 : (int64_t)((int)blockIdx.x - G) * a.chunk;
+  if (!merge && t_lo >= T) return;
+  const int t_hi = (int)min(t_lo + a.chunk, (int64_t)T);
   const float* lrow = a.logits + bh * a.max_T * G;
-  constexpr int kPer = kPoolChunk / kCombineThreads;  // tokens per thread
+  constexpr int kPer = kPoolBatch / kCombineThreads / (V > 1 ? V : 1);  // tokens per thread and batch
+  constexpr int kBatch = kPer * kCombineThreads;
   float4 x[V > 0 ? kPer : 1][V > 0 ? V : 1];
-  if (V > 0 && !merge) {
+  auto load = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int t = chunk * kPoolChunk + i * kCombineThreads + threadIdx.x;
+      const int t = t0 + i * kCombineThreads + threadIdx.x;
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        x[i][j] = t < T ? reinterpret_cast<const float4*>(lrow)[(int64_t)t * V + j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[i][j] = t < t_hi ? reinterpret_cast<const float4*>(lrow)[(int64_t)t * V + j] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  }
+  };
+  if (V > 0 && !merge) load((int)t_lo);
   // the slots of this unit: those of the blocks that hold its first stage to its last
   int64_t before;
   const int64_t total = line_length(a.seq_len, a.B, a.max_T, b, before) * a.Hkv;
@@ -892,21 +903,28 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   const float invG = 1.f / (float)G;
   // no finite score at all (every page entry bad): relative to 0 the probabilities are 0
   if constexpr (V > 0) {
+    float4 l[V];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = chunk * kPoolChunk + i * kCombineThreads + threadIdx.x;
-      float acc = 0.f;
+    for (int j = 0; j < V; ++j) l[j] = *reinterpret_cast<const float4*>(&s_lse2[4 * j]);
+    for (int t0 = (int)t_lo; t0 < t_hi; t0 += kBatch) {
+      float p[kPer];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float4 l = *reinterpret_cast<const float4*>(&s_lse2[4 * j]);
-        acc += (fast_exp2(x[i][j].x - l.x) + fast_exp2(x[i][j].y - l.y)) +
-               (fast_exp2(x[i][j].z - l.z) + fast_exp2(x[i][j].w - l.w));
+      for (int i = 0; i < kPer; ++i) {
+        p[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          p[i] += (fast_exp2(x[i][j].x - l[j].x) + fast_exp2(x[i][j].y - l[j].y)) +
+                  (fast_exp2(x[i][j].z - l[j].z) + fast_exp2(x[i][j].w - l[j].w));
       }
-      if (t < T) prow[t] = acc * invG;
+      load(t0 + kBatch);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t0 + i * kCombineThreads + threadIdx.x;
+        if (t < t_hi) prow[t] = p[i] * invG;
+      }
     }
   } else {
-    const int t_hi = (int)min((int64_t)(chunk + 1) * kPoolChunk, (int64_t)T);
-    for (int t = chunk * kPoolChunk + threadIdx.x; t < t_hi; t += kCombineThreads) {
+    for (int t = (int)t_lo + threadIdx.x; t < t_hi; t += kCombineThreads) {
       float acc = 0.f;
       for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - s_lse2[g]);
       prow[t] = acc * invG;
@@ -994,7 +1012,10 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.B = p.B; c.blocks = blocks;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
-  const dim3 cgrid(p.G + (p.max_T + kPoolChunk - 1) / kPoolChunk, p.Hkv, p.B);
+  // As many batches per block as leave about four blocks per SM.
+  const int64_t batches = ((int64_t)p.max_T + kPoolBatch - 1) / kPoolBatch * p.B * p.Hkv;
+  c.chunk = kPoolBatch * (int)std::min<int64_t>(16, std::max<int64_t>(1, batches / (4 * 148)));
+  const dim3 cgrid(p.G + (p.max_T + c.chunk - 1) / c.chunk, p.Hkv, p.B);
   return launch_overlapped(pick_combine(p.G, p.f16), cgrid, kCombineThreads, 0, st, c);
 }
 

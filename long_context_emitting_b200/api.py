@@ -251,11 +251,29 @@ def _need_rows(name: str, t, dtype: torch.dtype, shape: tuple) -> None:
         raise ValueError(f"{name} must have contiguous rows")
 
 
-def _need_one_device(t0: torch.Tensor, **others) -> None:
-    dev = t0.get_device()
-    for name, t in others.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {t0.device}")
+def _need_device(name: str, t: torch.Tensor, dev: int) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
+
+
+def _sized(name: str, t, dtype: torch.dtype, n: int, dev: int) -> int:
+    """The address of a tensor that passes _need_size and is on device ``dev``."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.numel() >= n
+            and t.is_contiguous()):
+        _need_size(name, t, dtype, n)
+        _need_device(name, t, dev)
+    return t.data_ptr()
+
+
+def _rows(name: str, t, dtype: torch.dtype, shape: tuple, dev: int):
+    """Address and strides of a tensor that passes _need_rows and is on device ``dev``."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        st = t.stride()
+        if st[-1] == 1:
+            return t.data_ptr(), st
+    _need_rows(name, t, dtype, shape)
+    _need_device(name, t, dev)
+    return t.data_ptr(), t.stride()
 
 
 # A decode step makes some of these calls for every layer: what a call does not have to build anew
@@ -264,11 +282,11 @@ _shape = functools.lru_cache(maxsize=256)(Shape)
 _strides = functools.lru_cache(maxsize=1024)(Strides)
 
 
-def _call(dev: torch.device, name: str, *args) -> None:
+def _call(dev: int, name: str, *args) -> None:
     """The entry point on the current stream of the tensors' device, which need
     not be the current device."""
     fn = getattr(_lib(), name)
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+    if dev < 0 or dev == torch.cuda.current_device():
         rc = fn(*args, _stream())
     else:
         with torch.cuda.device(dev):
@@ -276,29 +294,22 @@ def _call(dev: torch.device, name: str, *args) -> None:
     check(rc, name)
 
 
-def _span(t: torch.Tensor):
-    """First byte of a [., ., ., 128] view of 16-bit rows and the byte after its last."""
-    a = t.data_ptr()
-    (n0, n1, n2, n3), (s0, s1, s2, s3) = t.shape, t.stride()
-    return a, a + 2 * ((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + (n3 - 1) * s3 + 1)
+def _end(a: int, n0: int, n1: int, n2: int, st) -> int:
+    """The byte after the last of a [n0, n1, n2, 128] view of 16-bit rows at address a."""
+    return a + 2 * ((n0 - 1) * st[0] + (n1 - 1) * st[1] + (n2 - 1) * st[2] + HEAD_DIM)
 
 
-def _need_apart(ins, outs) -> None:
-    """Each output [B, H, N, 128] is one of the inputs [B, N, H, 128] exactly, or
-    shares no memory with any."""
-    spans = [_span(t) for t in ins]
-    for name, out in outs:
-        a, b = _span(out)
-        overlaps = False
-        for t, (lo, hi) in zip(ins, spans):
-            if lo < b and a < hi:
-                t = t.transpose(1, 2)
-                if lo == a and t.stride() == out.stride() and t.shape == out.shape:
-                    break
-                overlaps = True
-        else:
-            if overlaps:
-                raise ValueError(f"{name} overlaps an input without being the same view")
+def _need_apart(name: str, a: int, b: int, st, H: int, ins) -> None:
+    """An output [B, H, N, 128] at bytes a to b is one of the inputs [B, N, H, 128] exactly,
+    or shares no memory with any."""
+    overlaps = False
+    for lo, hi, s, heads in ins:
+        if lo < b and a < hi:
+            if lo == a and heads == H and (s[0], s[2], s[1]) == st[:3]:
+                return
+            overlaps = True
+    if overlaps:
+        raise ValueError(f"{name} overlaps an input without being the same view")
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -315,44 +326,45 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     also the inputs themselves (``q_out=q.transpose(1, 2)``).
     """
     B, N, Hq, d = q.shape
+    dt = q.dtype
     sfx = _data_suffix(q, k)
     Hkv = k.shape[2]
-    _need_rows("q", q, q.dtype, (B, N, Hq, d))
-    _need_rows("k", k, q.dtype, (B, N, Hkv, d))
-    _need_size("positions", positions, torch.int32, B * N)
-    _need_size("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need_size(name, w, q.dtype, d)
+    _need_rows("q", q, dt, (B, N, Hq, d))
+    dev = q.get_device()
+    qp, qs = q.data_ptr(), q.stride()
+    kp, ks = _rows("k", k, dt, (B, N, Hkv, d), dev)
+    pos = _sized("positions", positions, torch.int32, B * N, dev)
+    inv = _sized("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
+    qw = None if q_weight is None else _sized("q_weight", q_weight, dt, d, dev)
+    kw = None if k_weight is None else _sized("k_weight", k_weight, dt, d, dev)
     if q_out is None:
-        q_out = torch.empty(B, Hq, N, d, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(B, Hq, N, d, dtype=dt, device=q.device)
     if k_out is None:
-        k_out = torch.empty(B, Hkv, N, d, dtype=q.dtype, device=q.device)
-    _need_rows("q_out", q_out, q.dtype, (B, Hq, N, d))
-    _need_rows("k_out", k_out, q.dtype, (B, Hkv, N, d))
-    _need_one_device(q, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight,
-                     q_out=q_out, k_out=k_out)
+        k_out = torch.empty(B, Hkv, N, d, dtype=dt, device=q.device)
+    qop, qos = _rows("q_out", q_out, dt, (B, Hq, N, d), dev)
+    kop, kos = _rows("k_out", k_out, dt, (B, Hkv, N, d), dev)
     if B and N:
-        _need_apart((q, k), (("q_out", q_out), ("k_out", k_out)))
-    _call(q.device, "kascade_qk_norm_rope" + sfx, _shape(B, Hq, Hkv, d), N,
-          _ptr(q), _strides(*q.stride()[:3]), _ptr(k), _strides(*k.stride()[:3]), _ptr(positions), _ptr(inv_freq),
-          _ptr(q_weight), _ptr(k_weight), float(eps), int(bool(interleaved)),
-          _ptr(q_out), _strides(q_out.stride(0), q_out.stride(2), q_out.stride(1)),
-          _ptr(k_out), _strides(k_out.stride(0), k_out.stride(2), k_out.stride(1)))
+        ins = (qp, _end(qp, B, N, Hq, qs), qs, Hq), (kp, _end(kp, B, N, Hkv, ks), ks, Hkv)
+        _need_apart("q_out", qop, _end(qop, B, Hq, N, qos), qos, Hq, ins)
+        _need_apart("k_out", kop, _end(kop, B, Hkv, N, kos), kos, Hkv, ins)
+    _call(dev, "kascade_qk_norm_rope" + sfx, _shape(B, Hq, Hkv, d), N, qp, _strides(*qs[:3]), kp, _strides(*ks[:3]),
+          pos, inv, qw, kw, float(eps), 1 if interleaved else 0, qop, _strides(qos[0], qos[2], qos[1]),
+          kop, _strides(kos[0], kos[2], kos[1]))
     return q_out, k_out
 
 
 # ------------------------------------------------------ 4-bit paged cache ----
-def _need_pages_q4(kv_pages, block_table, B: int, Hkv: int, page_size: int) -> None:
-    """Store [num_pages, Hkv, page_size, 160] and a block table with a row of
-    page numbers for each of the B sequences."""
-    _need_cuda("kv_pages", kv_pages, torch.uint8)
-    _need_cuda("block_table", block_table, torch.int32)
-    if kv_pages.dim() != 4 or tuple(kv_pages.shape[1:]) != (Hkv, page_size, Q4_ROW_BYTES):
-        raise ValueError(
-            f"kv_pages must be [num_pages, {Hkv}, {page_size}, {Q4_ROW_BYTES}], got {tuple(kv_pages.shape)}")
-    if block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError(f"block_table must be [>= {B}, max_pages], got {tuple(block_table.shape)}")
+def _pages_q4(kv_pages, block_table, B: int, Hkv: int, page_size: int, dev: int):
+    """Address and number of pages of a store [num_pages, Hkv, page_size, 160], address and row
+    length of a block table with a row of page numbers for each of the B sequences."""
+    pages = _sized("kv_pages", kv_pages, torch.uint8, 0, dev)
+    table = _sized("block_table", block_table, torch.int32, 0, dev)
+    shape, rows = kv_pages.shape, block_table.shape
+    if len(shape) != 4 or shape[1:] != (Hkv, page_size, Q4_ROW_BYTES):
+        raise ValueError(f"kv_pages must be [num_pages, {Hkv}, {page_size}, {Q4_ROW_BYTES}], got {tuple(shape)}")
+    if len(rows) != 2 or rows[0] < B:
+        raise ValueError(f"block_table must be [>= {B}, max_pages], got {tuple(rows)}")
+    return pages, shape[0], table, rows[1]
 
 
 def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=None):
@@ -366,16 +378,15 @@ def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=
     B, Hkv, N, d = k.shape
     sfx = _data_suffix(k, v)
     _need_rows("k", k, k.dtype, (B, Hkv, N, d))
-    _need_rows("v", v, k.dtype, (B, Hkv, N, d))
-    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
-    _need_size("start", start, torch.int32, B)
-    if count is not None:
-        _need_size("count", count, torch.int32, B)
-    _need_one_device(k, v=v, kv_pages=kv_pages, block_table=block_table, start=start, count=count)
-    _call(k.device, "kascade_kv_write_paged_q4" + sfx, _shape(B, Hkv, Hkv, d), N,
-          _ptr(k), _strides(k.stride(0), k.stride(2), k.stride(1)),
-          _ptr(v), _strides(v.stride(0), v.stride(2), v.stride(1)), _ptr(kv_pages), kv_pages.shape[0],
-          _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count))
+    dev = k.get_device()
+    ks = k.stride()
+    vp, vs = _rows("v", v, k.dtype, (B, Hkv, N, d), dev)
+    pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
+    first = _sized("start", start, torch.int32, B, dev)
+    n = None if count is None else _sized("count", count, torch.int32, B, dev)
+    _call(dev, "kascade_kv_write_paged_q4" + sfx, _shape(B, Hkv, Hkv, d), N, k.data_ptr(),
+          _strides(ks[0], ks[2], ks[1]), vp, _strides(vs[0], vs[2], vs[1]), pages, num_pages, table, max_pages,
+          int(page_size), first, n)
     return kv_pages
 
 
@@ -389,18 +400,19 @@ def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int
     sfx = "_f16" if dtype == torch.float16 else ""
     if dtype not in _DATA_DTYPES:
         raise TypeError("dtype must be bfloat16 or float16")
-    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
-    _need_size("start", start, torch.int32, B)
-    if count is not None:
-        _need_size("count", count, torch.int32, B)
+    _need_cuda("kv_pages", kv_pages, torch.uint8)
+    dev = kv_pages.get_device()
+    pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
+    first = _sized("start", start, torch.int32, B, dev)
+    n = None if count is None else _sized("count", count, torch.int32, B, dev)
     k = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if k is None else k
     v = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if v is None else v
-    for name, t in (("k", k), ("v", v)):
-        _need_size(name, t, dtype, B * Hkv * N * HEAD_DIM)
-    _need_one_device(kv_pages, block_table=block_table, start=start, count=count, k=k, v=v)
-    _call(kv_pages.device, "kascade_kv_read_paged_q4" + sfx, _shape(B, Hkv, Hkv, HEAD_DIM), int(N), _ptr(kv_pages),
-          kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(start), _ptr(count),
-          _ptr(k), _ptr(v))
+    size = B * Hkv * N * HEAD_DIM
+    kp, vp = _sized("k", k, dtype, size, dev), _sized("v", v, dtype, size, dev)
+    if abs(kp - vp) < 2 * size:
+        raise ValueError("k and v share memory")
+    _call(dev, "kascade_kv_read_paged_q4" + sfx, _shape(B, Hkv, Hkv, HEAD_DIM), int(N), pages, num_pages, table, max_pages,
+          int(page_size), first, n, kp, vp)
     return k, v
 
 
@@ -414,26 +426,26 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     the _f16 entry point when q is float16)."""
     B, Hq, d = q.shape
     sfx = _data_suffix(q)
-    _need_cuda("q", q, q.dtype)
-    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
-    _need_size("seq_len", seq_len, torch.int32, B)
-    dev = q.device
+    dt = q.dtype
+    _need_cuda("q", q, dt)
+    dev = q.get_device()
+    pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
+    lens = _sized("seq_len", seq_len, torch.int32, B, dev)
     if ld_pooled is None:
         ld_pooled = (max_T + 3) // 4 * 4
-    out = torch.empty(B, Hq, d, dtype=q.dtype, device=dev) if out is None else out
-    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if lse is None else lse
-    pooled = torch.empty(B, Hkv, ld_pooled, dtype=torch.float32, device=dev) if pooled is None else pooled
-    _need_size("out", out, q.dtype, B * Hq * d)
-    _need_size("lse", lse, torch.float32, B * Hq)
-    _need_size("pooled", pooled, torch.float32, B * Hkv * ld_pooled)
+    out = torch.empty(B, Hq, d, dtype=dt, device=q.device) if out is None else out
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
+    pooled = torch.empty(B, Hkv, ld_pooled, dtype=torch.float32, device=q.device) if pooled is None else pooled
+    op = _sized("out", out, dt, B * Hq * d, dev)
+    lp = _sized("lse", lse, torch.float32, B * Hq, dev)
+    pp = _sized("pooled", pooled, torch.float32, B * Hkv * ld_pooled, dev)
     shape = _shape(B, Hq, Hkv, d)
     if ws is None:
-        ws = workspace(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T), dev)
-    _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, out=out, lse=lse,
-                     pooled=pooled, ws=ws)
-    _call(dev, "kascade_decode_anchor_paged_q4" + sfx, shape, _ptr(q), _ptr(kv_pages), kv_pages.shape[0],
-          _ptr(block_table), block_table.shape[1], int(page_size), _ptr(seq_len), int(max_T), float(scale),
-          _ptr(out), _ptr(lse), _ptr(pooled), int(ld_pooled), _ptr(ws), _ws_bytes(ws))
+        ws = workspace(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T), q.device)
+    ws_bytes = _ws_bytes(ws)
+    _need_device("ws", ws, dev)
+    _call(dev, "kascade_decode_anchor_paged_q4" + sfx, shape, q.data_ptr(), pages, num_pages, table, max_pages,
+          int(page_size), lens, int(max_T), float(scale), op, lp, pp, int(ld_pooled), ws.data_ptr(), ws_bytes)
     return out, lse, pooled
 
 
@@ -443,23 +455,21 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     the _f16 entry point when q is float16)."""
     B, Hq, d = q.shape
     sfx = _data_suffix(q)
-    _need_cuda("q", q, q.dtype)
-    _need_pages_q4(kv_pages, block_table, B, Hkv, page_size)
+    dt = q.dtype
+    _need_cuda("q", q, dt)
+    dev = q.get_device()
+    pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     k_max = idx.shape[-1]
-    _need_size("seq_len", seq_len, torch.int32, B)
-    _need_size("idx", idx, torch.int32, B * Hkv * k_max)
-    _need_size("idx_k", idx_k, torch.int32, B * Hkv)
-    _need_size("head_map", head_map, torch.int32, Hkv)
-    dev = q.device
-    out = torch.empty(B, Hq, d, dtype=q.dtype, device=dev) if out is None else out
-    lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if lse is None else lse
-    _need_size("out", out, q.dtype, B * Hq * d)
-    _need_size("lse", lse, torch.float32, B * Hq)
-    _need_one_device(q, kv_pages=kv_pages, block_table=block_table, seq_len=seq_len, idx=idx, idx_k=idx_k,
-                     head_map=head_map, out=out, lse=lse)
-    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, _shape(B, Hq, Hkv, d), _ptr(q), _ptr(kv_pages),
-          kv_pages.shape[0], _ptr(block_table), block_table.shape[1], int(page_size), _ptr(seq_len), _ptr(idx),
-          _ptr(idx_k), int(k_max), _ptr(head_map), float(scale), _ptr(out), _ptr(lse))
+    lens = _sized("seq_len", seq_len, torch.int32, B, dev)
+    ip = _sized("idx", idx, torch.int32, B * Hkv * k_max, dev)
+    np = _sized("idx_k", idx_k, torch.int32, B * Hkv, dev)
+    mp = _sized("head_map", head_map, torch.int32, Hkv, dev)
+    out = torch.empty(B, Hq, d, dtype=dt, device=q.device) if out is None else out
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
+    op = _sized("out", out, dt, B * Hq * d, dev)
+    lp = _sized("lse", lse, torch.float32, B * Hq, dev)
+    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, _shape(B, Hq, Hkv, d), q.data_ptr(), pages, num_pages, table,
+          max_pages, int(page_size), lens, ip, np, k_max, mp, float(scale), op, lp)
     return out, lse
 
 

@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   }
   __syncwarp();
 
-  int b, h, T, i_begin, i_end;
+  int b, h, T, i_begin, i_end, token_0 = 0;
+  const int step = GATHER ? (int)gridDim.x * kWarps * kStageRows : kStageRows;  // from one stage of a warp to its next
   const int32_t* sel = nullptr;
   int64_t left = 0;  // anchor: what this block still has of the line
   int at = 0;        // and where in its unit that starts
@@ -467,12 +468,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     sel = a.idx + (int64_t)row * a.k_max;
     if (!ok && threadIdx.x == 0 && blockIdx.x == 0) flag_status(a.status, kStatusBadIndex);
     if (!ok || T == 0) n_items = 0;  // nothing to gather from an empty sequence
-    // a row is shared out evenly over the cluster's warps, whatever its length
-    const int parts = (int)gridDim.x * kWarps;
-    const int per_warp = ((n_items + parts - 1) / parts + kStageRows - 1) / kStageRows * kStageRows;
-    const int64_t first = (int64_t)((int)blockIdx.x * kWarps + warp) * per_warp;
-    i_begin = (int)min(first, (int64_t)n_items);
-    i_end = (int)min(first + per_warp, (int64_t)n_items);
+    // the cluster's warps take the row's stages in turn: even shares, whatever its length
+    i_begin = ((int)blockIdx.x * kWarps + warp) * kStageRows;
+    i_end = n_items;
+    // the first indices do not wait for the row's length
+    token_0 = i_begin + lane < a.k_max ? __ldg(sel + i_begin + lane) : 0;
   } else {
     int64_t none;
     const int64_t total = line_length(a.seq_len, a.B, a.max_T, 0, none) * a.Hkv;
@@ -527,22 +527,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
   }
   const int64_t bh = (int64_t)b * a.Hkv + h;
-  const int n_iter = (i_end - i_begin + kStageRows - 1) / kStageRows;
+  const int n_iter = i_end > i_begin ? (i_end - i_begin + step - 1) / step : 0;
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
   // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
   // and neither is looked at before the next stage's turn.
   auto load_token = [&](int it) -> int {
-    const int i = i_begin + kStageRows * it + lane;
+    const int i = i_begin + step * it + lane;
     if (i >= i_end) return kNoToken;
     return GATHER ? __ldg(sel + i) : i;
   };
-  const int token_0 = load_token(0);  // on its way, as is the first page of the anchor, while q is
-  int token_2 = token_0, token_1 = kNoToken, page_1 = 0, page_index = 0;
+  // the first token (reuse) or page (anchor) is on its way while q is
+  int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0, page_index = 0;
   auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
     token_1 = token_2;
     if (GATHER && (token_1 < 0 || token_1 >= T)) {
-      bad |= i_begin + kStageRows * it + lane < i_end;
+      bad |= i_begin + step * it + lane < i_end;
       token_1 = kNoToken;
     }
     if (token_1 != kNoToken) {
@@ -765,25 +765,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
   }
   if constexpr (GATHER) {
-    // the splits of (b, h) are one cluster: rank 0 merges them through distributed shared memory
+    // the splits of (b, h) are one cluster: they merge through distributed shared memory
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    if (cluster.block_rank() == 0) {
-      const int ns = (int)cluster.num_blocks();
-      for (int g = 0; g < G; ++g) {
-        float M = -INFINITY, L = 0.f, acc = 0.f;
-        for (int r = 0; r < ns; ++r) M = fmaxf(M, *cluster.map_shared_rank(&sm_pm[g], r));
-        for (int r = 0; r < ns; ++r) {
-          const float f = fast_exp2(*cluster.map_shared_rank(&sm_pm[g], r) - finite_max(M));
-          L += f * *cluster.map_shared_rank(&sm_pl[g], r);
-          acc += f * *cluster.map_shared_rank(&sm_po[g][d], r);
-        }
-        a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
-        if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
+    const int ns = (int)cluster.num_blocks();
+    for (int g = (int)cluster.block_rank(); g < G; g += ns) {  // the blocks share the heads
+      float M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll 4
+      for (int r = 0; r < ns; ++r) M = fmaxf(M, *cluster.map_shared_rank(&sm_pm[g], r));
+#pragma unroll 4
+      for (int r = 0; r < ns; ++r) {
+        const float f = fast_exp2(*cluster.map_shared_rank(&sm_pm[g], r) - finite_max(M));
+        L += f * *cluster.map_shared_rank(&sm_pl[g], r);
+        acc += f * *cluster.map_shared_rank(&sm_po[g][d], r);
       }
+      a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
+      if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
     }
-    cluster.sync();  // peers keep their shared memory until rank 0 has read it
+    cluster.sync();  // peers keep their shared memory until all have read it
     return;
   }
   // the next unit; a warp that gave up takes its whole block along

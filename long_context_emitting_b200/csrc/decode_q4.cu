@@ -119,6 +119,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Asynchronous copy of 16 bytes (zeros where src_bytes is 0).  The 64-byte hint matters: a row is 160
+// bytes, and without it whole 128-byte lines came from memory, 256 bytes a row instead of 192
+// (105 against 80 MB for 16 sequences of 32K, 26.6 against 24.8 us).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::64B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(src_bytes), "l"(policy)
+               : "memory");
+}
+
 // d = a b: a product that starts a sum (the sums' registers need no zeros first).
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -571,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       for (int i = 0; i < 10; ++i) {
         const int u = lane + 2 * i, r = (u * 205) >> 11;  // (lane + 32 i) / 10 = r + 3 i
         const int pl = __shfl_sync(0xffffffffu, place, r + 3 * i);
-        cp_async16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
-                   pl >= 0 ? 16 : 0);
+        copy16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
+               pl >= 0 ? 16 : 0, policy);
       }
     } else if ((lane & 15) == 0) {
       // 16 tokens that start at a multiple of 16 lie in one page, one behind the other: two copies,

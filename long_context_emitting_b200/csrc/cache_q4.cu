@@ -126,18 +126,23 @@ __device__ __forceinline__ uint32_t codes(const uint4& w, float s, float m, floa
     most = fmaxf(most, fabsf(r[i]));
   }
   if (most >= s * (0.5f - 0x1p-15f) && s > 0.f) {  // without a range all codes are 0
+    if (s < 0x1p-120f) {  // 1 / s is out of range: quotients of scaled numbers
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (s < 0x1p-120f) {  // 1 / s is out of range: start from a quotient of scaled numbers
+      for (int i = 0; i < 8; ++i) {
         n[i] = rintf(((x[i] - m) * 0x1p64f) / (s * 0x1p64f));
         r[i] = fmaf(-n[i], s, x[i] - m);
       }
-      const float d = x[i] - m, back = d - x[i];
-      const float lost = (x[i] - (d - back)) + (-m - back);  // x - m is d + lost
-      const float over = fmaf(2.f, r[i], -s) + 2.f * lost, under = fmaf(2.f, r[i], s) + 2.f * lost;
-      const bool odd = (int)n[i] & 1;
-      if (over > 0.f || (over == 0.f && odd)) n[i] += 1.f;
-      if (under < 0.f || (under == 0.f && odd)) n[i] -= 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(r[i]) >= s * (0.5f - 0x1p-15f)) {
+        const float d = x[i] - m, back = d - x[i];
+        const float lost = (x[i] - (d - back)) + (-m - back);  // x - m is d + lost
+        const float side = copysignf(1.f, r[i]);
+        const float over = fmaf(2.f * lost, side, fmaf(2.f, fabsf(r[i]), -s));
+        const bool odd = __float_as_uint(n[i] + 0x1p23f) & 1u;
+        if (over > 0.f || (over == 0.f && odd)) n[i] += side;
+      }
     }
   }
   // four codes in 16 bits: exact in fp32, and read off the low bits after adding 2^23
@@ -241,6 +246,26 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a
   if (bad) flag_status(a.status, kStatusNonFinite);
 }
 
+// minimum + scale * code of the 8 codes in a word, in 16 bits.  A nibble at bit 4i, put below the
+// exponent of 2^23, is that number plus code · 16^i: nothing is shifted or converted.
+template <bool F16>
+__device__ __forceinline__ uint4 values(uint32_t w, float s, float m) {
+  float v[8];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t h = half ? w >> 16 : w;
+    float unit = s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float n = __uint_as_float((h & (15u << (4 * i))) | 0x4b000000u) - 0x1p23f;
+      v[4 * half + i] = fmaf(unit, n, m);
+      unit *= 0.0625f;
+    }
+  }
+  return make_uint4(pack_x2<F16>(v[0], v[1]), pack_x2<F16>(v[2], v[3]), pack_x2<F16>(v[4], v[5]),
+                    pack_x2<F16>(v[6], v[7]));
+}
+
 template <int TOK, bool F16>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a) {
   overlap_launches();
@@ -271,16 +296,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
 #pragma unroll
     for (int u = 0; u < 4; ++u) f[u] = __uint_as_float(__shfl_sync(0xffffffffu, tail, base + 4 * u + g) << 16);
     if (p.row >= 0 && h < p.h_end) {
-      uint32_t ok[4], ov[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        ok[u] = pack_x2<F16>(fmaf(f[0], (float)((kw >> (8 * u)) & 15u), f[1]),
-                             fmaf(f[0], (float)((kw >> (8 * u + 4)) & 15u), f[1]));
-        ov[u] = pack_x2<F16>(fmaf(f[2], (float)((vw >> (8 * u)) & 15u), f[3]),
-                             fmaf(f[2], (float)((vw >> (8 * u + 4)) & 15u), f[3]));
-      }
-      *reinterpret_cast<uint4*>(a.k_out + dst) = make_uint4(ok[0], ok[1], ok[2], ok[3]);
-      *reinterpret_cast<uint4*>(a.v_out + dst) = make_uint4(ov[0], ov[1], ov[2], ov[3]);
+      const uint4 ok = values<F16>(kw, f[0], f[1]), ov = values<F16>(vw, f[2], f[3]);
+      *reinterpret_cast<uint4*>(a.k_out + dst) = ok;
+      *reinterpret_cast<uint4*>(a.v_out + dst) = ov;
     }
     dst += (int64_t)kStep * a.N * kHeadDim;
     kw = nk;

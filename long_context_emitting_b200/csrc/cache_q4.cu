@@ -62,19 +62,19 @@ __device__ __forceinline__ uint32_t bf16_up_pos(float x) {  // x >= 0
   return ((u & 0xffffu) ? u + 0x10000u : u) >> 16;
 }
 
-// Minima of the halves of two words, in the data's type; a NaN stays.
-template <bool F16>
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+// Minima and maxima of the halves of two words, in the data's type; a NaN stays.
+template <bool F16, bool MAX>
+__device__ __forceinline__ uint32_t ends2(uint32_t a, uint32_t b) {
   if constexpr (F16) {
-    const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    const __half2 x = *reinterpret_cast<const __half2*>(&a), y = *reinterpret_cast<const __half2*>(&b);
+    const __half2 r = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
     return *reinterpret_cast<const uint32_t*>(&r);
   } else {
-    const __nv_bfloat162 r =
-        __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a), y = *reinterpret_cast<const __nv_bfloat162*>(&b);
+    const __nv_bfloat162 r = MAX ? __hmax2_nan(x, y) : __hmin2_nan(x, y);
     return *reinterpret_cast<const uint32_t*>(&r);
   }
 }
-constexpr uint32_t kSigns = 0x80008000u;
 
 __device__ __forceinline__ float approx_rcp(float x) {
   float y;
@@ -85,11 +85,11 @@ __device__ __forceinline__ float approx_rcp(float x) {
 // Minimum and minus maximum of the group's values, packed in the data's type.
 template <bool F16>
 __device__ __forceinline__ uint32_t group_ends(const uint4& w) {
-  const uint32_t lo = min2<F16>(min2<F16>(w.x, w.y), min2<F16>(w.z, w.w));
-  const uint32_t hi = min2<F16>(min2<F16>(w.x ^ kSigns, w.y ^ kSigns), min2<F16>(w.z ^ kSigns, w.w ^ kSigns));
-  uint32_t ends = min2<F16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-  ends = min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
-  return min2<F16>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+  const uint32_t lo = ends2<F16, false>(ends2<F16, false>(w.x, w.y), ends2<F16, false>(w.z, w.w));
+  const uint32_t hi = ends2<F16, true>(ends2<F16, true>(w.x, w.y), ends2<F16, true>(w.z, w.w)) ^ 0x80008000u;
+  uint32_t ends = ends2<F16, false>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+  ends = ends2<F16, false>(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+  return ends2<F16, false>(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
 }
 
 struct Scale {
@@ -186,7 +186,7 @@ struct Place {
 };
 
 template <int TOK, bool F16>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheArgs a) {
   overlap_launches();
   const Place<TOK> p(a);
   // whole warps leave together: a tile past the end of its sequence costs nothing more

@@ -337,11 +337,13 @@ __device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
 // Weights p · vs · c of this lane's rows a and b (layout of scores) as the B operands of the value
 // products, and the minima's sums.  `tail` is the address of row a's V scales.
 template <bool PAIR>
-__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], bool has_a, bool has_b,
+__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], uint32_t mask, int row,
                                         uint32_t (&ba)[4], uint32_t (&bb)[4]) {
   uint4 ta = lds128(tail), tb = lds128(tail + 8 * kQ4Row);
-  if (!has_a) ta = make_uint4(0, 0, 0, 0);  // p is 0 there, but 0 times a stray NaN is not
-  if (!has_b) tb = make_uint4(0, 0, 0, 0);
+  if (mask != 0xffffffffu) {  // p is 0 where there is no row, but 0 times a stray NaN is not
+    if (!((mask >> row) & 1u)) ta = make_uint4(0, 0, 0, 0);
+    if (!((mask >> (row + 8)) & 1u)) tb = make_uint4(0, 0, 0, 0);
+  }
   uint32_t top = 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -540,14 +542,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
   // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
-  // and neither is looked at before the next stage's turn.
+  // and neither is looked at before the next stage's turn.  The anchor needs one row per half stage: 16
+  // tokens that start at a multiple of 16 lie in one page, one behind the other.
   auto load_token = [&](int it) -> int {
-    const int i = i_begin + step * it + lane;
+    const int i = i_begin + step * it + (GATHER ? lane : lane & 16);
     if (i >= i_end) return kNoToken;
     return GATHER ? __ldg(sel + i) : i;
   };
   // the first token (reuse) or page (anchor) is on its way while q is
-  int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0, page_index = 0;
+  int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0,
+      page_index = 0;
   auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
     token_1 = token_2;
     if (GATHER && (token_1 < 0 || token_1 >= T)) {
@@ -563,32 +567,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   if (!GATHER) load_page(0);
   uint32_t masks[kStages];  // rows present, stage by stage in order of use
   auto issue = [&](int it, int st, uint32_t& mask) {
-    int place = -1;  // row of the page store
-    if (token_1 != kNoToken) {
-      place = (page_1 * a.Hkv + h) * a.page_size + (token_1 - page_index * a.page_size);
-      if ((unsigned)page_1 >= (unsigned)a.num_pages) {
-        bad = true;
-        place = -1;
-      }
-    }
-    load_page(it + 1);
-    mask = __ballot_sync(0xffffffffu, place >= 0);
+    const int place = (page_1 * a.Hkv + h) * a.page_size + (token_1 - page_index * a.page_size);  // in the page store
+    const bool here = token_1 != kNoToken, good = (unsigned)page_1 < (unsigned)a.num_pages;
+    bad |= here && !good;
     const uint32_t dst = ring + (uint32_t)st * kStageBytes;
     if constexpr (GATHER) {
+      const int row = here && good ? place : -1;
+      load_page(it + 1);
+      mask = __ballot_sync(0xffffffffu, row >= 0);
       // 320 chunks of 16 bytes, ten to a row; the two of a 32-byte sector go to neighbouring lanes
 #pragma unroll
       for (int i = 0; i < 10; ++i) {
         const int u = lane + 2 * i, r = (u * 205) >> 11;  // (lane + 32 i) / 10 = r + 3 i
-        const int pl = __shfl_sync(0xffffffffu, place, r + 3 * i);
+        const int pl = __shfl_sync(0xffffffffu, row, r + 3 * i);
         copy16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
                pl >= 0 ? 16 : 0, policy);
       }
-    } else if ((lane & 15) == 0) {
-      // 16 tokens that start at a multiple of 16 lie in one page, one behind the other: two copies,
-      // each announced by its own lane (of no bytes, where the rows are past the end or the page is bad)
-      const uint32_t bytes = (uint32_t)__popc((mask >> lane) & 0xffffu) * kQ4Row;
-      mbar_expect_tx(bar + 8 * st, bytes);
-      if (bytes) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, bytes, bar + 8 * st, policy);
+    } else {
+      const int rows = here && good ? min(i_end - token_1, 16) : 0;
+      load_page(it + 1);
+      mask = __ballot_sync(0xffffffffu, (lane & 15) < rows);
+      if ((lane & 15) == 0) {  // two copies, each announced by its own lane (of no bytes, where there are no rows)
+        mbar_expect_tx(bar + 8 * st, (uint32_t)rows * kQ4Row);
+        if (rows) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, (uint32_t)rows * kQ4Row,
+                            bar + 8 * st, policy);
+      }
     }
   };
 
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
   }
   float* lrow = a.logits + (bh * a.max_T + i_begin + (int)half + tok_a) * G + col;
-  const bool two_heads = !(G & 1) && col < G;  // one aligned store of both
+  const int64_t eight = 8 * G;  // logits of 8 tokens
   float base0 = 0.f, base1 = 0.f;              // finite_max of the maxima
 
 #pragma unroll
@@ -639,29 +642,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p24f * ((i & 1) ? qx.f1 : qx.f0);
     const bool full = mask == 0xffffffffu;
-    bool has[4] = {true, true, true, true};  // the lane's rows: a and b of each set
     if (!full) {
 #pragma unroll
-      for (int u = 0; u < 2 * kSets; ++u) {
-        has[u] = (mask >> (8 * u + half + tok_a)) & 1u;
-        if (!has[u]) s[u >> 1][2 * (u & 1)] = s[u >> 1][2 * (u & 1) + 1] = -INFINITY;
-      }
+      for (int u = 0; u < 2 * kSets; ++u)
+        if (!((mask >> (8 * u + half + tok_a)) & 1u)) s[u >> 1][2 * (u & 1)] = s[u >> 1][2 * (u & 1) + 1] = -INFINITY;
     }
     if constexpr (!GATHER) {
-      const int rest = i_end - (i_begin + kStageRows * it + (int)half + tok_a);
+      if (full && !(G & 1)) {
+        if (col < G) {
 #pragma unroll
-      for (int u = 0; u < 2 * kSets; ++u) {
-        float* p = lrow + 8 * u * G;
-        const float x0 = s[u >> 1][2 * (u & 1)], x1 = s[u >> 1][2 * (u & 1) + 1];
-        if (full || rest > 8 * u) {
-          if (two_heads) *reinterpret_cast<float2*>(p) = make_float2(x0, x1);
-          else {
-            if (col < G) p[0] = x0;
-            if (col + 1 < G) p[1] = x1;
+          for (int u = 0; u < 2 * kSets; ++u)
+            *reinterpret_cast<float2*>(lrow + u * eight) = make_float2(s[u >> 1][2 * (u & 1)], s[u >> 1][2 * (u & 1) + 1]);
+        }
+      } else {
+        const int rest = i_end - (i_begin + kStageRows * it + (int)half + tok_a);
+#pragma unroll
+        for (int u = 0; u < 2 * kSets; ++u) {
+          if (rest > 8 * u) {
+            if (col < G) lrow[u * eight] = s[u >> 1][2 * (u & 1)];
+            if (col + 1 < G) lrow[u * eight + 1] = s[u >> 1][2 * (u & 1) + 1];
           }
         }
       }
-      lrow += kStageRows * G;
+      lrow += 4 * eight;
     }
     float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
     if constexpr (!PAIR) {
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
       w.l0 += s[u][0] + s[u][2];
       w.l1 += s[u][1] + s[u][3];
-      weights<PAIR>(w, mine + 16 * u * kQ4Row + kQ4Tail + 16, s[u], has[2 * u], has[2 * u + 1], ba, bb);
+      weights<PAIR>(w, mine + 16 * u * kQ4Row + kQ4Tail + 16, s[u], mask, 16 * u + (int)half + tok_a, ba, bb);
       values(w, rows + 16 * u * kQ4Row, gid, tig, ba, bb);
     }
     if constexpr (PAIR) {
@@ -1021,9 +1024,10 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.B = p.B; c.blocks = blocks;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
-  // As many batches per block as leave about four blocks per SM.
-  const int64_t batches = ((int64_t)p.max_T + kPoolBatch - 1) / kPoolBatch * p.B * p.Hkv;
-  c.chunk = kPoolBatch * (int)std::min<int64_t>(16, std::max<int64_t>(1, batches / (4 * 148)));
+  // As many batches per block as leave about eight blocks per SM.
+  const int batch = p.G == 8 ? kPoolBatch / 2 : kPoolBatch;
+  const int64_t batches = ((int64_t)p.max_T + batch - 1) / batch * p.B * p.Hkv;
+  c.chunk = batch * (int)std::min<int64_t>(16, std::max<int64_t>(1, batches / (8 * 148)));
   const dim3 cgrid(p.G + (p.max_T + c.chunk - 1) / c.chunk, p.Hkv, p.B);
   return launch_overlapped(pick_combine(p.G, p.f16), cgrid, kCombineThreads, 0, st, c);
 }

@@ -80,7 +80,8 @@ struct Q4Args {
   int B;
   float scale_log2;
   float* logits;   // anchor: [B, Hkv, max_T, G] base-2 scaled logits
-  float* part_ml;  // [blocks + B*Hkv, G, 2], see Span
+  int2* parts;     // [B*Hkv]: first and last block of a unit
+  float* part_ml;  // [blocks + B*Hkv, G, 2]
   float* part_o;   // [blocks + B*Hkv, G, 128]
   uint16_t* out;   // reuse
   float* lse;
@@ -407,7 +408,7 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
 // batch of one long and many short sequences then keeps every SM busy to the end.  Starting and
 // merging a unit costs a block about as much as kUnitCost stages, so a unit is that much longer on
 // the line.  A block's part of unit u goes to slot block + u of the partial results: both only ever
-// grow along the line, so no two parts meet, and the combine kernel finds a unit's slots by arithmetic.
+// grow along the line, so no two parts meet, and a unit's slots follow one another.
 #ifndef Q4_UNIT_COST
 #define Q4_UNIT_COST 12
 #endif
@@ -419,16 +420,13 @@ __device__ __forceinline__ int length_of(int T, int max_T) {  // on the line
   const int n = stages_of(T, max_T);
   return n ? n + kUnitCost : 0;
 }
-// Length of all sequences and, in `before`, of the first b, for one key head.
-__device__ __forceinline__ int64_t line_length(const int32_t* seq_len, int B, int max_T, int b, int64_t& before) {
+// Length of all sequences, for one key head.
+__device__ __forceinline__ int64_t line_length(const int32_t* seq_len, int B, int max_T) {
   const int lane = threadIdx.x & 31;
   int64_t total = 0;
-  before = 0;
-  for (int i = 0; i < B; i += 32) {
-    const int n = i + lane < B ? length_of(seq_len[i + lane], max_T) : 0;
-    total += __reduce_add_sync(0xffffffffu, (unsigned)n);
-    before += __reduce_add_sync(0xffffffffu, (unsigned)(i + lane < b ? n : 0));
-  }
+#pragma unroll 4
+  for (int i = 0; i < B; i += 32)
+    total += __reduce_add_sync(0xffffffffu, (unsigned)(i + lane < B ? length_of(seq_len[i + lane], max_T) : 0));
   return total;
 }
 // Blocks that take part: each has some of the line, each warp has a stage where there are enough.
@@ -485,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     // the first indices do not wait for the row's length
     token_0 = i_begin + lane < a.k_max ? __ldg(sel + i_begin + lane) : 0;
   } else {
-    int64_t none;
-    const int64_t total = line_length(a.seq_len, a.B, a.max_T, 0, none) * a.Hkv;
+    const int64_t total = line_length(a.seq_len, a.B, a.max_T) * a.Hkv;
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < a.B; i += kThreads)
         if (a.seq_len[i] < 0 || a.seq_len[i] > a.max_T) flag_status(a.status, kStatusBadIndex);
@@ -534,6 +531,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     if (end <= max(at, kUnitCost)) return;  // nothing left, or no stage of the last unit
     left -= end - at;
     const int s0 = max(at - kUnitCost, 0), ns = end - kUnitCost - s0;
+    if (threadIdx.x == 0) {
+      int2* parts = a.parts + ((int64_t)b * a.Hkv + h);
+      if (s0 == 0) parts->x = (int)blockIdx.x;
+      if (s0 + ns == n) parts->y = (int)blockIdx.x;
+    }
     i_begin = (s0 + (int)((int64_t)ns * warp / kWarps)) * kStageRows;
     i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
   }
@@ -813,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 
 struct CombineArgs {
   const int32_t* seq_len;
-  int B, Hq, Hkv, G, max_T, blocks, chunk;  // blocks: grid of the first kernel
+  int Hq, Hkv, G, max_T, blocks, chunk;  // blocks: grid of the first kernel
+  const int2* parts;
   const float* part_ml;
   const float* part_o;
   const float* logits;
@@ -861,14 +864,13 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   };
   if (V > 0 && !merge) load((int)t_lo);
   // the slots of this unit: those of the blocks that hold its first stage to its last
-  int64_t before;
-  const int64_t total = line_length(a.seq_len, a.B, a.max_T, b, before) * a.Hkv;
-  const int mine = length_of(T, a.max_T), blocks = working_blocks(total, a.blocks);
   int c0 = 0, ns = 0;
-  if (mine) {
-    const int64_t first = before * a.Hkv + (int64_t)h * mine;  // block c starts at total c / blocks
-    c0 = (int)(((first + kUnitCost + 1) * blocks - 1) / total);
-    ns = (int)(((first + mine) * blocks - 1) / total) - c0 + 1;
+  if (T > 0) {
+    const int2 part = a.parts[bh];
+    if (part.x >= 0 && part.x <= part.y && part.y < a.blocks) {  // not so if the first kernel gave up
+      c0 = part.x;
+      ns = part.y - part.x + 1;
+    }
   }
   const float* ml = a.part_ml + (c0 + bh) * G * 2;
   if (merge ? warp == 0 : warp < G) {
@@ -958,7 +960,7 @@ int reuse_split(int64_t units, int k_max) {
 }
 
 struct WsLayout {
-  size_t logits, part_ml, part_o, total;
+  size_t logits, parts, part_ml, part_o, total;
 };
 WsLayout ws_layout(int B, int Hkv, int G, int max_T) {
   WsLayout w;
@@ -966,6 +968,8 @@ WsLayout ws_layout(int B, int Hkv, int G, int max_T) {
   size_t off = 0;
   w.logits = off;
   off = align_up(off + (size_t)B * Hkv * max_T * G * sizeof(float), 256);
+  w.parts = off;
+  off = align_up(off + (size_t)B * Hkv * sizeof(int2), 256);
   w.part_ml = off;
   off = align_up(off + slots * G * 2 * sizeof(float), 256);
   w.part_o = off;
@@ -1012,6 +1016,7 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   char* ws = static_cast<char*>(p.ws);
   Q4Args a = common_args(p);
   a.logits = reinterpret_cast<float*>(ws + w.logits);
+  a.parts = reinterpret_cast<int2*>(ws + w.parts);
   a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   auto kern = pick_kernel<false>(p.G <= 4, p.f16);
@@ -1021,7 +1026,8 @@ cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   CombineArgs c;
   c.seq_len = p.seq_len;
-  c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.B = p.B; c.blocks = blocks;
+  c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.max_T = p.max_T; c.blocks = blocks;
+  c.parts = a.parts;
   c.part_ml = a.part_ml; c.part_o = a.part_o; c.logits = a.logits;
   c.pooled = p.pooled; c.ld_pooled = p.ld_pooled; c.out = p.out; c.lse = p.lse;
   // As many batches per block as leave about eight blocks per SM.

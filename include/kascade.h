@@ -343,7 +343,8 @@ int kascade_qk_norm_rope_f16(kascade_shape s, int32_t N, const uint16_t* q,
  * skipped (KASCADE_ERR_BAD_INDEX in the device status).  A group that holds a NaN or an
  * infinity, or whose range exceeds the largest float, is stored as scale 0, minimum NaN, reads
  * back as NaN and sets KASCADE_ERR_NONFINITE.  Two tokens of one call must not share a slot.
- * s.Hq is not used; B·N <= 2^30, Hkv <= 4096.  The _f16 variants take fp16 rows; the pages
+ * s.Hq is not used; B·N <= 2^30, Hkv <= 4096, and a store has fewer than 2^31 rows
+ * (num_pages * Hkv * page_size; KASCADE_ERR_UNSUPPORTED_SHAPE).  The _f16 variants take fp16 rows; the pages
  * are the same. */
 #define KASCADE_Q4_ROW_BYTES 160
 int kascade_kv_write_paged_q4(kascade_shape s, int32_t N, const uint16_t* k,

@@ -286,12 +286,15 @@ def _call(dev: int, name: str, *args) -> None:
     """The entry point on the current stream of the tensors' device, which need
     not be the current device."""
     fn = getattr(_lib(), name)
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev < 0:
         rc = fn(*args, _stream())
+    elif dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream())
-    check(rc, name)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        check(rc, name)
 
 
 def _end(a: int, n0: int, n1: int, n2: int, st) -> int:

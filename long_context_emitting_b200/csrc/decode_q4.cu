@@ -39,6 +39,7 @@
 // 16-byte K reads (pairs of rows) and the 8-byte V reads (every second fragment
 // row) both meet different banks.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "q4.cuh"
 #include "tcgen05.cuh"
@@ -145,6 +146,12 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// bfloat16 number g of two words.
+__device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
+  const uint32_t w = g < 2 ? w01 : w23;
+  return (g & 1) ? bf16_hi(w) : bf16_lo(w);
+}
+
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -247,11 +254,16 @@ __device__ __forceinline__ void score_codes(float (&d)[4], uint32_t wa, uint32_t
   mma_f16_16816(d, low_nibbles(ua, ha), low_nibbles(ub, hb), ha, hb, q[2], q[3]);
 }
 
-// Scores of SETS x 16 rows at shared address `rows`, in units of 2^-24: c[0], c[1] are the lane's two
-// heads of its row a, c[2], c[3] of row b = a + 8.  `mine` is the address of the lane's own row a.
-template <bool PAIR>
+// Scores of 16 (PAIR: 32) rows at shared address `rows`, in units of 2^-24: c[0], c[1] are the lane's
+// two heads of its row a, c[2], c[3] of row b = a + 8.  `mine` is the address of the lane's own row a.
+// Groups and minima largely cancel, so partial sums are larger than the score, and an error of their
+// last bits would be a relative one of every probability.  With LOW `low` collects what the sums'
+// roundings left (per group (c - c') + s d, two heads per instruction): the pooled probabilities of
+// 128K tokens are then off by 0.8e-6 instead of 1.1e-6, for 4% of the anchor's time.  The reuse call,
+// which has no probabilities to give, goes without.
+template <bool PAIR, bool LOW>
 __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint32_t row_a, uint32_t mine, int tig,
-                                       uint32_t mask, int tok_a, float (&c)[4]) {
+                                       uint32_t mask, int tok_a, float (&c)[4], float (&low)[4]) {
   constexpr int kSets = PAIR ? 2 : 1;
   const uint2 sa = lds64(mine + kQ4Tail), sb = lds64(mine + 8 * kQ4Row + kQ4Tail);
   uint4 ka[kSets], kb[kSets];
@@ -268,17 +280,26 @@ __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint
     if (u == 0) mma_bf16_first(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
     else mma_bf16_16816(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
   }
+  uint64_t sum[2] = {f2_pack(c[0], c[1]), f2_pack(c[2], c[3])}, left[2] = {0, 0};
+  const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float d[4];
     score_codes<true>(d, word_of(ka[0], g), word_of(kb[0], g), x.b[0][g]);
     if constexpr (PAIR) score_codes<false>(d, word_of(ka[1], g), word_of(kb[1], g), x.b[1][g]);
-    const uint32_t wa = g < 2 ? sa.x : sa.y, wb = g < 2 ? sb.x : sb.y;
-    const float fa = (g & 1) ? bf16_hi(wa) : bf16_lo(wa), fb = (g & 1) ? bf16_hi(wb) : bf16_lo(wb);
-    c[0] = fmaf(fa, d[0], c[0]);
-    c[1] = fmaf(fa, d[1], c[1]);
-    c[2] = fmaf(fb, d[2], c[2]);
-    c[3] = fmaf(fb, d[3], c[3]);
+    const float fa = tail_at(sa.x, sa.y, g), fb = tail_at(sb.x, sb.y, g);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint64_t f = r ? f2_pack(fb, fb) : f2_pack(fa, fa), v = f2_pack(d[2 * r], d[2 * r + 1]);
+      const uint64_t next = f2_fma(f, v, sum[r]);
+      if constexpr (LOW) left[r] = f2_add(left[r], f2_fma(f, v, f2_fma(next, minus, sum[r])));
+      sum[r] = next;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    f2_unpack(sum[r], c[2 * r], c[2 * r + 1]);
+    f2_unpack(left[r], low[2 * r], low[2 * r + 1]);
   }
 }
 
@@ -329,77 +350,146 @@ __device__ __forceinline__ void rebase(State& w, int h, float al) {
   }
 }
 
-// bfloat16 number g of two words.
-__device__ __forceinline__ float tail_at(uint32_t w01, uint32_t w23, int g) {
-  const uint32_t w = g < 2 ? w01 : w23;
-  return (g & 1) ? bf16_hi(w) : bf16_lo(w);
-}
+// A stage's weights as the B operands of the value products: b[block of 16 rows][group], and with
+// LOW what their rounding to half precision left.  With PAIR that stands in the columns that have no
+// head (second[] is not used): columns 0..3 of block 0 hold the weights and 4..7 the rest, of block 1
+// the other way round; the merge adds the two.
+struct Weights {
+  uint32_t first[2][4][2], second[2][4][2];
+};
 
-// Weights p · vs · c of this lane's rows a and b (layout of scores) as the B operands of the value
-// products, and the minima's sums.  `tail` is the address of row a's V scales.
-template <bool PAIR>
-__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[4], uint32_t mask, int row,
-                                        uint32_t (&ba)[4], uint32_t (&bb)[4]) {
-  uint4 ta = lds128(tail), tb = lds128(tail + 8 * kQ4Row);
-  if (mask != 0xffffffffu) {  // p is 0 where there is no row, but 0 times a stray NaN is not
-    if (!((mask >> row) & 1u)) ta = make_uint4(0, 0, 0, 0);
-    if (!((mask >> (row + 8)) & 1u)) tb = make_uint4(0, 0, 0, 0);
+// p: exponentials of the lane's rows a and b (layout of scores), of each set of rows.  `tail` is the
+// address of the first row a's V scales.  Also adds the minima's sums.
+template <bool PAIR, bool LOW>
+__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[PAIR ? 1 : 2][4], uint32_t mask, int row,
+                                        int tig, Weights& out) {
+  constexpr int kSets = PAIR ? 1 : 2;
+  uint4 t[kSets][2];
+#pragma unroll
+  for (int u = 0; u < 2 * kSets; ++u) {
+    uint4& x = t[u >> 1][u & 1];
+    x = lds128(tail + 8 * u * kQ4Row);
+    // p is 0 where there is no row, but 0 times a stray NaN is not
+    if (mask != 0xffffffffu && !((mask >> (row + 8 * u)) & 1u)) x = make_uint4(0, 0, 0, 0);
   }
-  uint32_t top = 0;
+  uint32_t hi[kSets][4][2], lo[kSets][4][2], top = 0;
+  auto pack = [&](int g) {
+#pragma unroll
+    for (int u = 0; u < 2 * kSets; ++u) {
+      const float f = tail_at(t[u >> 1][u & 1].x, t[u >> 1][u & 1].y, g);
+      const float* q = &p[u >> 1][2 * (u & 1)];
+      const float w0 = q[0] * w.c[g][0] * f, w1 = q[1] * w.c[g][1] * f;
+      const uint32_t h = pack_f16x2(w0, w1);
+      hi[u >> 1][g][u & 1] = h;
+      if constexpr (LOW) {
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        lo[u >> 1][g][u & 1] = pack_f16x2(w0 - back.x, w1 - back.y);
+      }
+    }
+  };
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
-    ba[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
-    bb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
-    top = __vimax3_u16x2(top, ba[g], bb[g]);  // halves that are not negative compare as integers
+    pack(g);
+#pragma unroll
+    for (int u = 0; u < kSets; ++u) top = __vimax3_u16x2(top, hi[u][g][0], hi[u][g][1]);  // not negative: as integers
   }
   if (__any_sync(0xffffffffu, (top & 0xffffu) >= 0x7800u || top >= 0x78000000u)) {
     // A weight has reached 2^15: factors that put the largest weight of such a head and group in
     // [2^7, 2^8).  A weight that is not finite spoils its own sums and moves no factor.
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float fa = tail_at(ta.x, ta.y, g), fb = tail_at(tb.x, tb.y, g);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float xa = p[h] * fa, xb = p[2 + h] * fb;
-        const float x = head_max<PAIR>(fmaxf(xa < INFINITY ? xa : 0.f, xb < INFINITY ? xb : 0.f));
+        float x = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2 * kSets; ++u) {
+          const float y = p[u >> 1][2 * (u & 1) + h] * tail_at(t[u >> 1][u & 1].x, t[u >> 1][u & 1].y, g);
+          x = fmaxf(x, y < INFINITY ? y : 0.f);
+        }
+        x = head_max<PAIR>(x);
         if (x * w.c[g][h] >= 0x1p15f) {
           const int n = 127 + 7 + 127 - max(exponent_of(x), 27);  // c stays within 2^107
           scale_sums(w, g, h, biased_pow2(127 + n - exponent_of(w.c[g][h])));
           w.c[g][h] = biased_pow2(n);
         }
       }
-      ba[g] = pack_f16x2(p[0] * w.c[g][0] * fa, p[1] * w.c[g][1] * fa);
-      bb[g] = pack_f16x2(p[2] * w.c[g][0] * fb, p[3] * w.c[g][1] * fb);
+      pack(g);
     }
   }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const float za = tail_at(ta.z, ta.w, g), zb = tail_at(tb.z, tb.w, g);
-    w.z[g][0] = fmaf(p[0], za, fmaf(p[2], zb, w.z[g][0]));
-    w.z[g][1] = fmaf(p[1], za, fmaf(p[3], zb, w.z[g][1]));
-    ba[g] = movmatrix_trans(ba[g]);
-    bb[g] = movmatrix_trans(bb[g]);
+#pragma unroll
+    for (int u = 0; u < kSets; ++u) {
+      const float za = tail_at(t[u][0].z, t[u][0].w, g), zb = tail_at(t[u][1].z, t[u][1].w, g);
+      w.z[g][0] = fmaf(p[u][0], za, fmaf(p[u][2], zb, w.z[g][0]));
+      w.z[g][1] = fmaf(p[u][1], za, fmaf(p[u][3], zb, w.z[g][1]));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (PAIR && LOW) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, lo[0][g][i], 2);
+        out.first[0][g][i] = movmatrix_trans(tig < 2 ? hi[0][g][i] : other);
+        out.first[1][g][i] = movmatrix_trans(tig < 2 ? other : hi[0][g][i]);
+      } else if constexpr (PAIR) {
+        // the second rows' weights stand in columns 4..7: swap them to 0..3 (4..7 of the sums are not used)
+        out.first[0][g][i] = movmatrix_trans(hi[0][g][i]);
+        out.first[1][g][i] = __shfl_xor_sync(0xffffffffu, out.first[0][g][i], 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+          out.first[u][g][i] = movmatrix_trans(hi[u][g][i]);
+          if constexpr (LOW) out.second[u][g][i] = movmatrix_trans(lo[u][g][i]);
+        }
+      }
+    }
   }
 }
 
-// O += V P for the 16 rows at `rows`.
-__device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig, const uint32_t (&ba)[4],
-                                       const uint32_t (&bb)[4]) {
-  // V rows of this lane's k pairs: fragment rows 2 tig, 2 tig + 1 and those + 8
-  const uint32_t v0 = rows + (uint32_t)tig * kQ4Row + kQ4V + 8 * gid;
-  const uint32_t v1 = rows + (uint32_t)(4 + (tig ^ 2)) * kQ4Row + kQ4V + 8 * gid;
-  const uint2 e0 = lds64(v0), e1 = lds64(v1), e2 = lds64(v0 + 8 * kQ4Row), e3 = lds64(v1 + 8 * kQ4Row);
+// O += V P for the 32 rows at `rows`.  The products of a stage start from zero and are added to the
+// sums in fp32: the matrix unit cuts each product off at the last bit of the sum that it joins, always
+// toward zero, and 2000 products of one sign would be 2^-15 short, which the minima, summed apart,
+// would not be (at 128K tokens 0.5% of the output).
+template <bool SECOND>
+__device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig, const Weights& b) {
+  uint2 e[2][4];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    // V rows of this lane's k pairs: fragment rows 2 tig, 2 tig + 1 and those + 8
+    const uint32_t v0 = rows + (uint32_t)(16 * u + tig) * kQ4Row + kQ4V + 8 * gid;
+    const uint32_t v1 = rows + (uint32_t)(16 * u + 4 + (tig ^ 2)) * kQ4Row + kQ4V + 8 * gid;
+    e[u][0] = lds64(v0);
+    e[u][1] = lds64(v1);
+    e[u][2] = lds64(v0 + 8 * kQ4Row);
+    e[u][3] = lds64(v1 + 8 * kQ4Row);
+  }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // half g % 2 of both rows' words
-    // whole bytes, and their high nibbles: the merge takes the difference of the two sums
-    uint32_t x = __byte_perm(g < 2 ? e0.x : e0.y, g < 2 ? e1.x : e1.y, sel);
-    uint32_t y = __byte_perm(g < 2 ? e2.x : e2.y, g < 2 ? e3.x : e3.y, sel);
-    mma_f16_16816(w.o[g][0], x & 0x00ff00ffu, x & 0x00f000f0u, y & 0x00ff00ffu, y & 0x00f000f0u, ba[g], bb[g]);
-    x = upper_bytes(x);
-    y = upper_bytes(y);
-    mma_f16_16816(w.o[g][1], x, x & 0x00f000f0u, y, y & 0x00f000f0u, ba[g], bb[g]);
+    float d[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      // whole bytes, and their high nibbles: the merge takes the difference of the two sums
+      const uint32_t x = __byte_perm(g < 2 ? e[u][0].x : e[u][0].y, g < 2 ? e[u][1].x : e[u][1].y, sel);
+      const uint32_t y = __byte_perm(g < 2 ? e[u][2].x : e[u][2].y, g < 2 ? e[u][3].x : e[u][3].y, sel);
+      const uint32_t a0 = x & 0x00ff00ffu, a1 = x & 0x00f000f0u, a2 = y & 0x00ff00ffu, a3 = y & 0x00f000f0u;
+      const uint32_t b0 = upper_bytes(x), b1 = b0 & 0x00f000f0u, b2 = upper_bytes(y), b3 = b2 & 0x00f000f0u;
+      if (u == 0) {
+        mma_f16_first(d[0], a0, a1, a2, a3, b.first[u][g][0], b.first[u][g][1]);
+        mma_f16_first(d[1], b0, b1, b2, b3, b.first[u][g][0], b.first[u][g][1]);
+      } else {
+        mma_f16_16816(d[0], a0, a1, a2, a3, b.first[u][g][0], b.first[u][g][1]);
+        mma_f16_16816(d[1], b0, b1, b2, b3, b.first[u][g][0], b.first[u][g][1]);
+      }
+      if constexpr (SECOND) {
+        mma_f16_16816(d[0], a0, a1, a2, a3, b.second[u][g][0], b.second[u][g][1]);
+        mma_f16_16816(d[1], b0, b1, b2, b3, b.second[u][g][0], b.second[u][g][1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w.o[g][0][i] += d[0][i];
+      w.o[g][1][i] += d[1][i];
+    }
   }
 }
 
@@ -636,13 +726,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     const uint32_t mask = masks[0];
     constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
     const uint32_t mine = rows + half * kQ4Row + row_a;
-    float s[kSets][4];
-    scores<PAIR>(qx, rows, row_a, mine, tig, mask, tok_a, s[0]);
-    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1]);
+    float s[kSets][4], low[kSets][4];
+    scores<PAIR, !GATHER>(qx, rows, row_a, mine, tig, mask, tok_a, s[0], low[0]);
+    if constexpr (!PAIR) scores<PAIR, !GATHER>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1], low[1]);
 #pragma unroll
     for (int u = 0; u < kSets; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p24f * ((i & 1) ? qx.f1 : qx.f0);
+      for (int i = 0; i < 4; ++i) {
+        const float f = (i & 1) ? qx.f1 : qx.f0;
+        s[u][i] = GATHER ? s[u][i] * 0x1p24f * f : fmaf(s[u][i] * 0x1p24f, f, low[u][i] * 0x1p24f * f);
+      }
     const bool full = mask == 0xffffffffu;
     if (!full) {
 #pragma unroll
@@ -685,25 +778,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       rebase(w, 0, al0);
       rebase(w, 1, al1);
     }
-    uint32_t ba[4], bb[4];
 #pragma unroll
     for (int u = 0; u < kSets; ++u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
       w.l0 += s[u][0] + s[u][2];
       w.l1 += s[u][1] + s[u][3];
-      weights<PAIR>(w, mine + 16 * u * kQ4Row + kQ4Tail + 16, s[u], mask, 16 * u + (int)half + tok_a, ba, bb);
-      values(w, rows + 16 * u * kQ4Row, gid, tig, ba, bb);
     }
-    if constexpr (PAIR) {
-      // the second rows' weights stand in columns 4..7: swap them to 0..3 (4..7 of the sums are not used)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        ba[g] = __shfl_xor_sync(0xffffffffu, ba[g], 16);
-        bb[g] = __shfl_xor_sync(0xffffffffu, bb[g], 16);
-      }
-      values(w, rows + 16 * kQ4Row, gid, tig, ba, bb);
-    }
+    // A half-precision output is rounded no more coarsely than a weight: there the weights get a second term.
+    Weights b;
+    weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, mask, (int)half + tok_a, tig, b);
+    values<!PAIR && F16>(w, rows, gid, tig, b);
     __syncwarp();  // the stage is read: it may be refilled
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
@@ -730,6 +815,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   __syncthreads();
   float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
   const bool owner = !PAIR || tig < 2;
+  if constexpr (PAIR && F16) {  // columns 4..7 hold the weights' second terms
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float& o = w.o[i >> 3][(i >> 2) & 1][i & 3];
+      o += __shfl_xor_sync(0xffffffffu, o, 2);
+    }
+  }
   if (gid == 0 && owner) {
     sm_m[warp][col] = w.m0;
     sm_m[warp][col + 1] = w.m1;
@@ -836,8 +928,8 @@ constexpr int kPoolBatch = 1024;  // tokens of a block in flight; a block has so
 template <bool F16, int V>
 __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(const CombineArgs a) {
   overlap_launches();
-  __shared__ float s_M[8], s_L[8];
-  __shared__ __align__(16) float s_lse2[8];
+  __shared__ float s_L[8];
+  __shared__ __align__(16) float s_M[8], s_inv[8];
   __shared__ float4 s_o[kCombineThreads / 32][kHeadDim / 4];
   const int b = blockIdx.z, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -885,7 +977,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
     if (lane == 0) {
       s_M[g] = finite_max(M);
       s_L[g] = L;
-      s_lse2[g] = merge ? lse2_of(M, L) : finite_max(lse2_of(M, L));
+      // probabilities are exp2(s - M) / L: a log-sum-exp is off by half its last bit, which all would share
+      s_inv[g] = L == 0.f ? 0.f : 1.f / (L * (float)G);  // no score at all: probabilities 0
     }
   }
   __syncthreads();
@@ -910,16 +1003,17 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
       for (int i = 0; i < kCombineThreads / 32; ++i) o += reinterpret_cast<const float*>(s_o[i])[threadIdx.x];
       a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + threadIdx.x] = to_bits<F16>(s_L[g] == 0.f ? 0.f : o / s_L[g]);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = s_lse2[g] * kLn2;
+    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(s_L[g] == 0.f ? -INFINITY : s_M[g], s_L[g]) * kLn2;
     return;
   }
   float* prow = a.pooled + bh * a.ld_pooled;
-  const float invG = 1.f / (float)G;
-  // no finite score at all (every page entry bad): relative to 0 the probabilities are 0
   if constexpr (V > 0) {
-    float4 l[V];
+    float4 m[V], f[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = *reinterpret_cast<const float4*>(&s_lse2[4 * j]);
+    for (int j = 0; j < V; ++j) {
+      m[j] = *reinterpret_cast<const float4*>(&s_M[4 * j]);
+      f[j] = *reinterpret_cast<const float4*>(&s_inv[4 * j]);
+    }
     for (int t0 = (int)t_lo; t0 < t_hi; t0 += kBatch) {
       float p[kPer];
 #pragma unroll
@@ -927,21 +1021,21 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
         p[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          p[i] += (fast_exp2(x[i][j].x - l[j].x) + fast_exp2(x[i][j].y - l[j].y)) +
-                  (fast_exp2(x[i][j].z - l[j].z) + fast_exp2(x[i][j].w - l[j].w));
+          p[i] += (fast_exp2(x[i][j].x - m[j].x) * f[j].x + fast_exp2(x[i][j].y - m[j].y) * f[j].y) +
+                  (fast_exp2(x[i][j].z - m[j].z) * f[j].z + fast_exp2(x[i][j].w - m[j].w) * f[j].w);
       }
       load(t0 + kBatch);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int t = t0 + i * kCombineThreads + threadIdx.x;
-        if (t < t_hi) prow[t] = p[i] * invG;
+        if (t < t_hi) prow[t] = p[i];
       }
     }
   } else {
     for (int t = (int)t_lo + threadIdx.x; t < t_hi; t += kCombineThreads) {
       float acc = 0.f;
-      for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - s_lse2[g]);
-      prow[t] = acc * invG;
+      for (int g = 0; g < G; ++g) acc += fast_exp2(lrow[(int64_t)t * G + g] - s_M[g]) * s_inv[g];
+      prow[t] = acc;
     }
   }
 }

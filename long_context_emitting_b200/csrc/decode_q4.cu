@@ -8,38 +8,45 @@
 // same for its 32 channels, so
 //   q · K_t    = sum_g [ ks_{t,g} (q_g · n_{t,g}) + km_{t,g} sum(q_g) ]
 //   out_d      = sum_t (p_t vs_{t,g}) n_{t,d}  +  sum_t p_t vm_{t,g}      (d in group g)
-// and mma.sync multiplies the codes n themselves: a nibble masked into the low
-// or the next four bits of a half word is the half-precision subnormal n · 2^-24
-// or n · 2^-20, exact, so eight codes cost one shift and four ANDs.  The other
-// operand carries the powers of two: q (scaled per head so that its largest
-// element is near 2^14; a bfloat16 or half q is then exact in half precision
-// down to 2^-29 of that) and p · vs (below).
+// and mma.sync multiplies the codes n themselves: a nibble in bits 4..7 of a half
+// word is the half-precision subnormal n · 2^-20, exact.  (tcgen05 would want the
+// codes unpacked into shared or tensor memory first: 512 bytes written and read
+// again per row of 160.)  The other operand carries the powers of two: q (scaled
+// per head so that its largest element is near 2^14; a bfloat16 or half q is then
+// exact in half precision down to 2^-28 of that) and p · vs (below).
 //   * S^T[16 tokens x 8 heads]: two m16n8k16 per scale group, whose fp32 sums
 //     the row's scales weight; the minima come in by one more mma, bfloat16
 //     minima against sum(q_g) split into three bfloat16 terms (24 bits).
-//   * O^T[128 channels x 8 heads]: per group the weights p · vs, rounded to half
-//     precision (at most 2^-11 of each weight, independently: as fine as a half
-//     output's rounding before it averages over the tokens), are the B operand.
-//     Weights of different tokens may differ by any power of two, so each head
-//     and group has its own factor c, a power of two: the first weights, and any
-//     that would pass 2^15, are put near 2^8, where weights 2^22 times smaller
-//     still keep all their bits.  When the running maximum moves, c takes up the
-//     change and the sums stay.  The minima are summed in fp32 (8 sums per lane).
+//   * O^T[128 channels x 8 heads]: per group the weights p · vs in half precision
+//     are the B operand: at most 2^-11 of each weight is lost, which against a
+//     bfloat16 output's 2^-8 does not show; for a half-precision output what is
+//     lost is a second operand.  Weights of different tokens may differ by any
+//     power of two, so each head and group has its own factor c, a power of two:
+//     the first weights, and any that would pass 2^15, are put near 2^8, where
+//     weights 2^22 times smaller still keep all their bits.  When the running
+//     maximum moves, c takes up the change and the sums stay.  The minima are
+//     summed in fp32 (8 sums per lane).
 //   * The running maximum moves only when a score exceeds it by 8 (weights then
-//     reach 2^8 instead of 1), so most blocks need one vote instead of a
-//     reduction and a rescale of the sums.
+//     reach 2^8 instead of 1), so most stages need one vote instead of a
+//     reduction and a rescale of the sums.  Values up to 2^100 are safe from
+//     overflow on the way.
+//   * Up to 4 heads fill half the columns.  The other half then serves the second
+//     16 rows of a stage (scores) or the weights' second terms (half precision).
 //
-// What bounds it: the cache's bytes (160 per token and key head) and, close
-// behind, instruction issue: about 270 warp instructions per 16 tokens.  A warp
-// owns a run of tokens and a ring of 32-row stages in shared memory that bulk
-// copies fill: 16 tokens from a page boundary are 2560 adjacent bytes, so the
-// anchor's stage is two copies; a reuse stage is 32 copies of one row.  No
-// registers hold data in flight.  Rows lie 160 bytes apart, which is 8 banks
-// mod 32; the fragment rows are taken in the order 0 6 1 7 2 4 3 5 so that the
-// 16-byte K reads (pairs of rows) and the 8-byte V reads (every second fragment
-// row) both meet different banks.
+// What bounds it, on one B200 (16 sequences of 32K, 32 heads on 8, bfloat16): the
+// first kernel reads 671 MB in 136 us, 4.9 TB/s; loads and scores alone take
+// 115 us, so memory comes first and 600 warp instructions per 32 rows (half of
+// them on the half-rate logic pipe, for picking nibbles out) stand close behind.  A
+// warp owns a run of rows and a ring of two 32-row stages in shared memory that
+// bulk copies fill: a half stage is 2560 adjacent bytes.  No registers hold data
+// in flight, and three blocks of four warps per SM leave each thread 168: with
+// four blocks and 128 registers it was 10% slower, with a third stage no faster.
+// A reuse stage is 32 rows of 160 bytes by 16-byte copies, two lanes to a sector;
+// one bulk copy per row took 51 instead of 34 us.  Rows lie 160 bytes apart, which is
+// 8 banks mod 32; the fragment rows are taken in the order 0 6 1 7 2 4 3 5 so
+// that the 16-byte K reads (pairs of rows) and the 8-byte V reads (every second
+// fragment row) both meet different banks.
 #include "common.cuh"
-#include "f32x2.cuh"
 #include "internal.h"
 #include "q4.cuh"
 #include "tcgen05.cuh"
@@ -163,7 +170,7 @@ template <bool PAIR>
 struct Query {
   uint32_t b[PAIR ? 2 : 1][4][4];  // per scale group: the two k16 steps' b0, b1
   uint32_t s[PAIR ? 2 : 1][2];     // sum(q_g) against the minima
-  float f0, f1;                    // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^24)
+  float f0, f1;                    // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^20)
 };
 
 template <bool PAIR, bool F16>
@@ -200,12 +207,9 @@ __device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, in
     }
     sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
     sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-    sum[g] *= 0x1p-24f;  // the codes' unit
-    // code j of a word is in half j / 4; odd j carry 16 times their code
-    x.b[0][g][0] = pack_f16x2(v[g][0], v[g][4]);
-    x.b[0][g][1] = pack_f16x2(v[g][1] * 0.0625f, v[g][5] * 0.0625f);
-    x.b[0][g][2] = pack_f16x2(v[g][2], v[g][6]);
-    x.b[0][g][3] = pack_f16x2(v[g][3] * 0.0625f, v[g][7] * 0.0625f);
+    sum[g] *= 0x1p-20f;  // the codes' unit
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.b[0][g][i] = pack_f16x2(v[g][i], v[g][i + 4]);  // code j of a word is in half j / 4
   }
   // k = 0..3: leading term of sum_g against minimum g, 4..7: second, 8..11: third, 12..15: nothing
   const float u0 = (tig & 1) ? sum[2] : sum[0], u1 = (tig & 1) ? sum[3] : sum[1];
@@ -237,33 +241,24 @@ __device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, in
 
 // Bytes 1 and 3 of w as two half words.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
-// b - hi of half-precision subnormals (exact): the low nibbles of bytes whose high ones are hi.  On
-// the multiply-add pipe, which has more room than that of the logic operations.
-__device__ __forceinline__ uint32_t low_nibbles(uint32_t b, uint32_t hi) {
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&hi));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-
-// Products of the codes in words wa and wb (of a lane's rows a and b) with the query.
+// Products of the codes in words wa and wb (of a lane's rows a and b) with the query.  Every nibble is
+// brought to bits 4..7 of its half word: the matrix unit lines products up by the operands' exponents,
+// which for a subnormal number say nothing of its leading zeros, and so many bits the sum then lacks.
+// (With half of the nibbles at bits 0..3 the log-sum-exp was off by 2e-7 instead of 5e-8.)
 template <bool FIRST>
 __device__ __forceinline__ void score_codes(float (&d)[4], uint32_t wa, uint32_t wb, const uint32_t (&q)[4]) {
-  const uint32_t la = wa & 0x000f000fu, lb = wb & 0x000f000fu, ga = wa & 0x00f000f0u, gb = wb & 0x00f000f0u;
-  if constexpr (FIRST) mma_f16_first(d, la, lb, ga, gb, q[0], q[1]);
-  else mma_f16_16816(d, la, lb, ga, gb, q[0], q[1]);
-  const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb), ha = ua & 0x00f000f0u, hb = ub & 0x00f000f0u;
-  mma_f16_16816(d, low_nibbles(ua, ha), low_nibbles(ub, hb), ha, hb, q[2], q[3]);
+  constexpr uint32_t kNibble = 0x00f000f0u;
+  if constexpr (FIRST) mma_f16_first(d, (wa << 4) & kNibble, (wb << 4) & kNibble, wa & kNibble, wb & kNibble, q[0], q[1]);
+  else mma_f16_16816(d, (wa << 4) & kNibble, (wb << 4) & kNibble, wa & kNibble, wb & kNibble, q[0], q[1]);
+  const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb);
+  mma_f16_16816(d, (ua << 4) & kNibble, (ub << 4) & kNibble, ua & kNibble, ub & kNibble, q[2], q[3]);
 }
 
-// Scores of 16 (PAIR: 32) rows at shared address `rows`, in units of 2^-24: c[0], c[1] are the lane's
+// Scores of 16 (PAIR: 32) rows at shared address `rows`, in units of 2^-20: c[0], c[1] are the lane's
 // two heads of its row a, c[2], c[3] of row b = a + 8.  `mine` is the address of the lane's own row a.
-// Groups and minima largely cancel, so partial sums are larger than the score, and an error of their
-// last bits would be a relative one of every probability.  With LOW `low` collects what the sums'
-// roundings left (per group (c - c') + s d, two heads per instruction): the pooled probabilities of
-// 128K tokens are then off by 0.8e-6 instead of 1.1e-6, for 4% of the anchor's time.  The reuse call,
-// which has no probabilities to give, goes without.
-template <bool PAIR, bool LOW>
+template <bool PAIR>
 __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint32_t row_a, uint32_t mine, int tig,
-                                       uint32_t mask, int tok_a, float (&c)[4], float (&low)[4]) {
+                                       uint32_t mask, int tok_a, float (&c)[4]) {
   constexpr int kSets = PAIR ? 2 : 1;
   const uint2 sa = lds64(mine + kQ4Tail), sb = lds64(mine + 8 * kQ4Row + kQ4Tail);
   uint4 ka[kSets], kb[kSets];
@@ -280,26 +275,16 @@ __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint
     if (u == 0) mma_bf16_first(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
     else mma_bf16_16816(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
   }
-  uint64_t sum[2] = {f2_pack(c[0], c[1]), f2_pack(c[2], c[3])}, left[2] = {0, 0};
-  const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     float d[4];
     score_codes<true>(d, word_of(ka[0], g), word_of(kb[0], g), x.b[0][g]);
     if constexpr (PAIR) score_codes<false>(d, word_of(ka[1], g), word_of(kb[1], g), x.b[1][g]);
     const float fa = tail_at(sa.x, sa.y, g), fb = tail_at(sb.x, sb.y, g);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint64_t f = r ? f2_pack(fb, fb) : f2_pack(fa, fa), v = f2_pack(d[2 * r], d[2 * r + 1]);
-      const uint64_t next = f2_fma(f, v, sum[r]);
-      if constexpr (LOW) left[r] = f2_add(left[r], f2_fma(f, v, f2_fma(next, minus, sum[r])));
-      sum[r] = next;
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    f2_unpack(sum[r], c[2 * r], c[2 * r + 1]);
-    f2_unpack(left[r], low[2 * r], low[2 * r + 1]);
+    c[0] = fmaf(fa, d[0], c[0]);
+    c[1] = fmaf(fa, d[1], c[1]);
+    c[2] = fmaf(fb, d[2], c[2]);
+    c[3] = fmaf(fb, d[3], c[3]);
   }
 }
 
@@ -726,16 +711,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     const uint32_t mask = masks[0];
     constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
     const uint32_t mine = rows + half * kQ4Row + row_a;
-    float s[kSets][4], low[kSets][4];
-    scores<PAIR, !GATHER>(qx, rows, row_a, mine, tig, mask, tok_a, s[0], low[0]);
-    if constexpr (!PAIR) scores<PAIR, !GATHER>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1], low[1]);
+    float s[kSets][4];
+    scores<PAIR>(qx, rows, row_a, mine, tig, mask, tok_a, s[0]);
+    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1]);
 #pragma unroll
     for (int u = 0; u < kSets; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = (i & 1) ? qx.f1 : qx.f0;
-        s[u][i] = GATHER ? s[u][i] * 0x1p24f * f : fmaf(s[u][i] * 0x1p24f, f, low[u][i] * 0x1p24f * f);
-      }
+      for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p20f * ((i & 1) ? qx.f1 : qx.f0);
     const bool full = mask == 0xffffffffu;
     if (!full) {
 #pragma unroll

@@ -47,6 +47,7 @@
 // that the 16-byte K reads (pairs of rows) and the 8-byte V reads (every second
 // fragment row) both meet different banks.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "q4.cuh"
 #include "tcgen05.cuh"
@@ -363,7 +364,10 @@ __device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p
     for (int u = 0; u < 2 * kSets; ++u) {
       const float f = tail_at(t[u >> 1][u & 1].x, t[u >> 1][u & 1].y, g);
       const float* q = &p[u >> 1][2 * (u & 1)];
-      const float w0 = q[0] * w.c[g][0] * f, w1 = q[1] * w.c[g][1] * f;
+      float w0, w1;
+      f2_unpack(f2_mul(f2_pack(q[0], q[1]), f2_pack(w.c[g][0], w.c[g][1])), w0, w1);
+      w0 *= f;
+      w1 *= f;
       const uint32_t h = pack_f16x2(w0, w1);
       hi[u >> 1][g][u & 1] = h;
       if constexpr (LOW) {
@@ -430,6 +434,10 @@ __device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p
   }
 }
 
+__device__ __forceinline__ void add2(float& x, float& y, float dx, float dy) {
+  f2_unpack(f2_add(f2_pack(x, y), f2_pack(dx, dy)), x, y);
+}
+
 // O += V P for the 32 rows at `rows`.  The products of a stage start from zero and are added to the
 // sums in fp32: the matrix unit cuts each product off at the last bit of the sum that it joins, always
 // toward zero, and 2000 products of one sign would be 2^-15 short, which the minima, summed apart,
@@ -471,9 +479,9 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w.o[g][0][i] += d[0][i];
-      w.o[g][1][i] += d[1][i];
+    for (int i = 0; i < 4; i += 2) {
+      add2(w.o[g][0][i], w.o[g][0][i + 1], d[0][i], d[0][i + 1]);
+      add2(w.o[g][1][i], w.o[g][1][i + 1], d[1][i], d[1][i + 1]);
     }
   }
 }

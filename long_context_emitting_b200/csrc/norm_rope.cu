@@ -15,7 +15,12 @@
 // What bounds it: memory (a row is read and written once, 4 bytes per channel
 // in all).  A row is 8 lanes x two 16-byte chunks, channels 8j.. and 64 + 8j..,
 // so both halves of a half-split pair are in one lane and nothing is exchanged
-// but the sum of squares.
+// but the sum of squares; the lane's eight cosines and sines stay in registers
+// over all heads, and the next rows are on their way while some are worked on.
+// Measured on one B200: 16384 tokens x 40 heads, bfloat16 with norms, 61.5 us,
+// 5.46 TB/s (83% of a plain copy's rate).  Four tokens per block: with eight the
+// same, with sixteen 82 us (too few blocks); two passes of rows ahead 67 us.
+// One token of 16 sequences takes 3.3 us, little more than an empty launch.
 #include "common.cuh"
 #include "internal.h"
 #include "q4.cuh"

@@ -492,10 +492,7 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
 // merging a unit costs a block about as much as kUnitCost stages, so a unit is that much longer on
 // the line.  A block's part of unit u goes to slot block + u of the partial results: both only ever
 // grow along the line, so no two parts meet, and a unit's slots follow one another.
-#ifndef Q4_UNIT_COST
-#define Q4_UNIT_COST 12
-#endif
-constexpr int kUnitCost = Q4_UNIT_COST;
+constexpr int kUnitCost = 12;  // a ragged batch: 52 us with 4, 43 with 8, 42 with 16
 __device__ __forceinline__ int stages_of(int T, int max_T) {
   return T > 0 && T <= max_T ? (T + kStageRows - 1) / kStageRows : 0;
 }
@@ -503,12 +500,12 @@ __device__ __forceinline__ int length_of(int T, int max_T) {  // on the line
   const int n = stages_of(T, max_T);
   return n ? n + kUnitCost : 0;
 }
-// Length of all sequences, for one key head.
-__device__ __forceinline__ int64_t line_length(const int32_t* seq_len, int B, int max_T) {
+// Length of all sequences, for one key head.  `mine` is the length of sequence `lane`, loaded before.
+__device__ __forceinline__ int64_t line_length(const int32_t* seq_len, int B, int max_T, int mine) {
   const int lane = threadIdx.x & 31;
-  int64_t total = 0;
+  int64_t total = __reduce_add_sync(0xffffffffu, (unsigned)length_of(mine, max_T));
 #pragma unroll 4
-  for (int i = 0; i < B; i += 32)
+  for (int i = 32; i < B; i += 32)
     total += __reduce_add_sync(0xffffffffu, (unsigned)(i + lane < B ? length_of(seq_len[i + lane], max_T) : 0));
   return total;
 }
@@ -566,7 +563,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     // the first indices do not wait for the row's length
     token_0 = i_begin + lane < a.k_max ? __ldg(sel + i_begin + lane) : 0;
   } else {
-    const int64_t total = line_length(a.seq_len, a.B, a.max_T) * a.Hkv;
+    const int mine = lane < a.B ? a.seq_len[lane] : 0;
+    const int64_t total = line_length(a.seq_len, a.B, a.max_T, mine) * a.Hkv;
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < a.B; i += kThreads)
         if (a.seq_len[i] < 0 || a.seq_len[i] > a.max_T) flag_status(a.status, kStatusBadIndex);
@@ -574,10 +572,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     if ((int)blockIdx.x >= blocks) return;
     const int64_t lo = total * blockIdx.x / blocks;
     left = total * (blockIdx.x + 1) / blocks - lo;
-    b = h = 0;
+    b = h = T = 0;
     int64_t base = 0;
     for (int i = 0; i < a.B; i += 32) {  // the sequence that holds lo
-      const int n = i + lane < a.B ? length_of(a.seq_len[i + lane], a.max_T) : 0;
+      const int len = i == 0 ? mine : i + lane < a.B ? a.seq_len[i + lane] : 0, n = length_of(len, a.max_T);
       int64_t end = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -590,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
         const int l = __ffs(past) - 1;
         const int64_t in = lo - (__shfl_sync(0xffffffffu, end, l) - (int64_t)__shfl_sync(0xffffffffu, n, l) * a.Hkv);
         const int per = __shfl_sync(0xffffffffu, n, l);
+        T = __shfl_sync(0xffffffffu, len, l);
         b = i + l;
         h = (int)(in / per);
         at = (int)(in - (int64_t)h * per);
@@ -609,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 
   while (true) {
   if constexpr (!GATHER) {
-    T = a.seq_len[b];
     const int n = stages_of(T, a.max_T), end = (int)min((int64_t)at + left, (int64_t)(n + kUnitCost));
     if (end <= max(at, kUnitCost)) return;  // nothing left, or no stage of the last unit
     left -= end - at;
@@ -652,7 +650,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   if (!GATHER) load_page(0);
   uint32_t masks[kStages];  // rows present, stage by stage in order of use
   auto issue = [&](int it, int st, uint32_t& mask) {
-    const int place = (page_1 * a.Hkv + h) * a.page_size + (token_1 - page_index * a.page_size);  // in the page store
+    // in the page store; of no meaning (and so unsigned) unless the token and its page are good
+    const int place = (int)(((uint32_t)page_1 * (uint32_t)a.Hkv + (uint32_t)h) * (uint32_t)a.page_size +
+                            ((uint32_t)token_1 - (uint32_t)page_index * (uint32_t)a.page_size));
     const bool here = token_1 != kNoToken, good = (unsigned)page_1 < (unsigned)a.num_pages;
     bad |= here && !good;
     const uint32_t dst = ring + (uint32_t)st * kStageBytes;
@@ -888,9 +888,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   at = 0;
   if (++h == a.Hkv) {
     h = 0;
-    do ++b;
-    while (b < a.B && stages_of(a.seq_len[b], a.max_T) == 0);
-    if (b == a.B) return;
+    do {
+      if (++b == a.B) return;
+      T = a.seq_len[b];
+    } while (stages_of(T, a.max_T) == 0);
   }
   }
 }
@@ -926,6 +927,7 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   const int G = a.G;
   const int64_t bh = (int64_t)b * a.Hkv + h;
   int T = a.seq_len[b];
+  const int2 part = a.parts[bh];  // of no meaning for an empty sequence
   if (T < 0 || T > a.max_T) T = 0;
   const bool merge = blockIdx.x < G;
   const int64_t t_lo = merge ? 0 : (int64_t)((int)blockIdx.x - G) * a.chunk;
@@ -948,7 +950,6 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   // the slots of this unit: those of the blocks that hold its first stage to its last
   int c0 = 0, ns = 0;
   if (T > 0) {
-    const int2 part = a.parts[bh];
     if (part.x >= 0 && part.x <= part.y && part.y < a.blocks) {  // not so if the first kernel gave up
       c0 = part.x;
       ns = part.y - part.x + 1;

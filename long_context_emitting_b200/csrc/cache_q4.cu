@@ -27,6 +27,7 @@
 // (2.7 TB/s; 350 warp instructions per two rows, so the issue slots, 74% busy,
 // come before memory), read back 28 us (5.0 TB/s).
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "q4.cuh"
 
@@ -121,12 +122,16 @@ __device__ __forceinline__ uint32_t codes(const uint4& w, float s, float m, floa
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack2<F16>(word_of(w, i), x[2 * i], x[2 * i + 1]);
+  // two channels per instruction
+  const uint64_t minus_m = f2_pack(-m, -m), inv2 = f2_pack(inv, inv), minus_s = f2_pack(-s, -s);
+  const uint64_t magic = f2_pack(0x1.8p23f, 0x1.8p23f), minus_magic = f2_pack(-0x1.8p23f, -0x1.8p23f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - m;
-    n[i] = fmaf(d, inv, 0x1.8p23f) - 0x1.8p23f;  // rounds to an integer
-    r[i] = fmaf(-n[i], s, d);
-    most = fmaxf(most, fabsf(r[i]));
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t d = f2_add(f2_pack(x[i], x[i + 1]), minus_m);
+    const uint64_t whole = f2_add(f2_fma(d, inv2, magic), minus_magic);  // rounds to integers
+    f2_unpack(whole, n[i], n[i + 1]);
+    f2_unpack(f2_fma(whole, minus_s, d), r[i], r[i + 1]);
+    most = fmax3(most, fabsf(r[i]), fabsf(r[i + 1]));
   }
   if (most >= s * (0.5f - 0x1p-15f) && s > 0.f) {  // without a range all codes are 0
     if (s < 0x1p-120f) {  // 1 / s is out of range: quotients of scaled numbers

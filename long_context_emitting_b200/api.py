@@ -59,12 +59,13 @@ _DATA_DTYPES = (torch.bfloat16, torch.float16)
 def _data_suffix(*ts) -> str:
     """'' for bfloat16 q/k/v/out, '_f16' for float16 (all of one call alike)."""
     dt = ts[0].dtype
-    same = dt in _DATA_DTYPES
+    sfx = "" if dt is torch.bfloat16 else "_f16" if dt is torch.float16 else None
     for t in ts:
-        same = same and t.dtype == dt
-    if not same:
+        if t.dtype is not dt:
+            sfx = None
+    if sfx is None:
         raise TypeError("q, k, v must all be bfloat16 or all float16")
-    return "_f16" if dt == torch.float16 else ""
+    return sfx
 
 
 def _stream() -> int:
@@ -288,7 +289,7 @@ def _call(dev: int, name: str, *args) -> None:
     fn = getattr(_lib(), name)
     if dev < 0:
         rc = fn(*args, _stream())
-    elif dev == torch.cuda.current_device():
+    elif dev == torch._C._cuda_getDevice():  # the tensors' checks have seen to it that CUDA is up
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -444,9 +445,11 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     pp = _sized("pooled", pooled, torch.float32, B * Hkv * ld_pooled, dev)
     shape = _shape(B, Hq, Hkv, d)
     if ws is None:
-        ws = workspace(_lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T), q.device)
-    ws_bytes = _ws_bytes(ws)
-    _need_device("ws", ws, dev)
+        ws_bytes = max(16, _lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T))
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    else:
+        ws_bytes = _ws_bytes(ws)
+        _need_device("ws", ws, dev)
     _call(dev, "kascade_decode_anchor_paged_q4" + sfx, shape, q.data_ptr(), pages, num_pages, table, max_pages,
           int(page_size), lens, int(max_T), float(scale), op, lp, pp, int(ld_pooled), ws.data_ptr(), ws_bytes)
     return out, lse, pooled

@@ -23,8 +23,8 @@
 // two groups into one word.  A block takes 16 tokens (fewer when there are few)
 // through several heads, so that a token's page is looked up once and the next
 // head's rows are on their way while one head's are worked on.
-// Measured on one B200, 26162 tokens x 8 heads in half precision: write 51 us
-// (2.7 TB/s; 350 warp instructions per two rows, so the issue slots, 74% busy,
+// Measured on one B200, 26162 tokens x 8 heads in half precision: write 48 us
+// (2.9 TB/s; 320 warp instructions per two rows, so the issue slots, 74% busy,
 // come before memory), read back 28 us (5.0 TB/s).
 #include "common.cuh"
 #include "f32x2.cuh"

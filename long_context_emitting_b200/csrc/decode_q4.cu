@@ -34,9 +34,9 @@
 //     16 rows of a stage (scores) or the weights' second terms (half precision).
 //
 // What bounds it, on one B200 (16 sequences of 32K, 32 heads on 8, bfloat16): the
-// first kernel reads 671 MB in 136 us, 4.9 TB/s; loads and scores alone take
-// 115 us, so memory comes first and 600 warp instructions per 32 rows (half of
-// them on the half-rate logic pipe, for picking nibbles out) stand close behind.  A
+// first kernel reads 671 MB in 136 to 145 us (by box), 4.6 to 4.9 TB/s; loads and
+// scores alone take 115 us, which is memory.  The rest is the 640 warp instructions
+// per 32 rows, half of them on the half-rate logic pipe to pick nibbles out.  A
 // warp owns a run of rows and a ring of two 32-row stages in shared memory that
 // bulk copies fill: a half stage is 2560 adjacent bytes.  No registers hold data
 // in flight, and three blocks of four warps per SM leave each thread 168: with

@@ -259,7 +259,7 @@ __device__ __forceinline__ void score_codes(float (&d)[4], uint32_t wa, uint32_t
 // two heads of its row a, c[2], c[3] of row b = a + 8.  `mine` is the address of the lane's own row a.
 template <bool PAIR>
 __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint32_t row_a, uint32_t mine, int tig,
-                                       uint32_t mask, int tok_a, float (&c)[4]) {
+                                       float (&c)[4]) {
   constexpr int kSets = PAIR ? 2 : 1;
   const uint2 sa = lds64(mine + kQ4Tail), sb = lds64(mine + 8 * kQ4Row + kQ4Tail);
   uint4 ka[kSets], kb[kSets];
@@ -268,11 +268,7 @@ __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint
     const uint32_t a = rows + 16 * u * kQ4Row + row_a, b = a + 8 * kQ4Row;
     ka[u] = lds128(a + 16 * tig);
     kb[u] = lds128(b + 16 * tig);
-    uint32_t ma = lds32(a + kQ4Tail + 8 + 4 * (tig & 1)), mb = lds32(b + kQ4Tail + 8 + 4 * (tig & 1));
-    if (PAIR && mask != 0xffffffffu) {  // what is left of older rows times the zeros of a column may be NaN
-      if (!((mask >> (16 * u + tok_a)) & 1u)) ma = 0;
-      if (!((mask >> (16 * u + tok_a + 8)) & 1u)) mb = 0;
-    }
+    const uint32_t ma = lds32(a + kQ4Tail + 8 + 4 * (tig & 1)), mb = lds32(b + kQ4Tail + 8 + 4 * (tig & 1));
     if (u == 0) mma_bf16_first(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
     else mma_bf16_16816(c, ma, mb, ma, mb, x.s[u][0], x.s[u][1]);
   }
@@ -347,17 +343,12 @@ struct Weights {
 // p: exponentials of the lane's rows a and b (layout of scores), of each set of rows.  `tail` is the
 // address of the first row a's V scales.  Also adds the minima's sums.
 template <bool PAIR, bool LOW>
-__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[PAIR ? 1 : 2][4], uint32_t mask, int row,
-                                        int tig, Weights& out) {
+__device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[PAIR ? 1 : 2][4], int tig,
+                                        Weights& out) {
   constexpr int kSets = PAIR ? 1 : 2;
   uint4 t[kSets][2];
 #pragma unroll
-  for (int u = 0; u < 2 * kSets; ++u) {
-    uint4& x = t[u >> 1][u & 1];
-    x = lds128(tail + 8 * u * kQ4Row);
-    // p is 0 where there is no row, but 0 times a stray NaN is not
-    if (mask != 0xffffffffu && !((mask >> (row + 8 * u)) & 1u)) x = make_uint4(0, 0, 0, 0);
-  }
+  for (int u = 0; u < 2 * kSets; ++u) t[u >> 1][u & 1] = lds128(tail + 8 * u * kQ4Row);
   uint32_t hi[kSets][4][2], lo[kSets][4][2], top = 0;
   auto pack = [&](int g) {
 #pragma unroll
@@ -717,16 +708,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
     const uint32_t rows = ring + (uint32_t)st * kStageBytes;
     const uint32_t mask = masks[0];
+    const bool full = mask == 0xffffffffu;
+    if (!GATHER && !full) {
+      // Rows that are not there become zeros (the reuse's copies have seen to that): whatever stands there
+      // would meet weights of 0 and columns of zeros, and 0 times a stray NaN is not 0.
+      for (int i = lane; i < (int)kStageBytes / 16; i += 32)
+        if (!((mask >> (i / 10)) & 1u)) sts128(rows + 16 * i, make_uint4(0, 0, 0, 0));
+      fence_proxy_async_smem();  // copies come to the same place later
+      __syncwarp();
+    }
     constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
     const uint32_t mine = rows + half * kQ4Row + row_a;
     float s[kSets][4];
-    scores<PAIR>(qx, rows, row_a, mine, tig, mask, tok_a, s[0]);
-    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, mask, tok_a, s[1]);
+    scores<PAIR>(qx, rows, row_a, mine, tig, s[0]);
+    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, s[1]);
 #pragma unroll
     for (int u = 0; u < kSets; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p20f * ((i & 1) ? qx.f1 : qx.f0);
-    const bool full = mask == 0xffffffffu;
     if (!full) {
 #pragma unroll
       for (int u = 0; u < 2 * kSets; ++u)
@@ -777,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
     // A half-precision output is rounded no more coarsely than a weight: there the weights get a second term.
     Weights b;
-    weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, mask, (int)half + tok_a, tig, b);
+    weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, tig, b);
     values<!PAIR && F16>(w, rows, gid, tig, b);
     __syncwarp();  // the stage is read: it may be refilled
 #pragma unroll

@@ -122,9 +122,11 @@ __device__ __forceinline__ uint64_t read_once_policy() {
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                          uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
 }
@@ -175,7 +177,8 @@ struct Query {
 };
 
 template <bool PAIR, bool F16>
-__device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, int G, float scale_log2, int gid, int tig) {
+__device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, int G, float scale_log2, int gid,
+                                           int tig) {
   float v[4][8];
   float top = 0.f;
 #pragma unroll
@@ -242,6 +245,7 @@ __device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, in
 
 // Bytes 1 and 3 of w as two half words.
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
+
 // Products of the codes in words wa and wb (of a lane's rows a and b) with the query.  Every nibble is
 // brought to bits 4..7 of its half word: the matrix unit lines products up by the operands' exponents,
 // which for a subnormal number say nothing of its leading zeros, and so many bits the sum then lacks.
@@ -249,8 +253,9 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t w) { return __byte_perm
 template <bool FIRST>
 __device__ __forceinline__ void score_codes(float (&d)[4], uint32_t wa, uint32_t wb, const uint32_t (&q)[4]) {
   constexpr uint32_t kNibble = 0x00f000f0u;
-  if constexpr (FIRST) mma_f16_first(d, (wa << 4) & kNibble, (wb << 4) & kNibble, wa & kNibble, wb & kNibble, q[0], q[1]);
-  else mma_f16_16816(d, (wa << 4) & kNibble, (wb << 4) & kNibble, wa & kNibble, wb & kNibble, q[0], q[1]);
+  const uint32_t la = (wa << 4) & kNibble, lb = (wb << 4) & kNibble;
+  if constexpr (FIRST) mma_f16_first(d, la, lb, wa & kNibble, wb & kNibble, q[0], q[1]);
+  else mma_f16_16816(d, la, lb, wa & kNibble, wb & kNibble, q[0], q[1]);
   const uint32_t ua = upper_bytes(wa), ub = upper_bytes(wb);
   mma_f16_16816(d, (ua << 4) & kNibble, (ub << 4) & kNibble, ua & kNibble, ub & kNibble, q[2], q[3]);
 }
@@ -288,7 +293,8 @@ __device__ __forceinline__ void scores(const Query<PAIR>& x, uint32_t rows, uint
 // Running state of a warp.  A lane's heads are 2 tig, 2 tig + 1 (PAIR: 2 (tig & 1) and the next).
 struct State {
   float m0, m1, l0, l1;
-  float o[4][2][4];  // [group][channel pair]: rows gid = channel 4 gid + 2 pair + 16 times the next, gid + 8 = the latter
+  // [group][channel pair]: rows gid = channel 4 gid + 2 pair + 16 times the next one, gid + 8 = the latter
+  float o[4][2][4];
   float z[4][2];     // sums of p · vm, this lane's rows
   float c[4][2];     // [group][head]: the sums o and the weights that enter them are times this power of two
 };
@@ -505,9 +511,8 @@ __device__ __forceinline__ int working_blocks(int64_t length, int blocks) {
   return (int)min((int64_t)blocks, (length + kWarps - 1) / kWarps);
 }
 
-// PAIR: at most 4 query heads per key head.  They are in columns 0..3 and again in 4..7, and after
-// the scores the lanes of columns 4..7 work on the second 16 rows of a stage: exponentials, weights
-// and minima then cost half.
+// PAIR: at most 4 query heads per key head.  The scores of a stage's first 16 rows are in columns 0..3
+// and those of the second in 4..7 (see Query), so exponentials, weights and minima cost half.
 template <bool GATHER, bool PAIR, bool F16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q4Args a) {
   // (clusters of the next reuse call, were they let in early, would leave some SMs to fewer of its blocks)
@@ -598,300 +603,302 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   bool alive = true, bad = false;  // bad: an index or page out of range was met
 
   while (true) {
-  if constexpr (!GATHER) {
-    const int n = stages_of(T, a.max_T), end = (int)min((int64_t)at + left, (int64_t)(n + kUnitCost));
-    if (end <= max(at, kUnitCost)) return;  // nothing left, or no stage of the last unit
-    left -= end - at;
-    const int s0 = max(at - kUnitCost, 0), ns = end - kUnitCost - s0;
-    if (threadIdx.x == 0) {
-      int2* parts = a.parts + ((int64_t)b * a.Hkv + h);
-      if (s0 == 0) parts->x = (int)blockIdx.x;
-      if (s0 + ns == n) parts->y = (int)blockIdx.x;
-    }
-    i_begin = (s0 + (int)((int64_t)ns * warp / kWarps)) * kStageRows;
-    i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
-  }
-  const int64_t bh = (int64_t)b * a.Hkv + h;
-  const int n_iter = i_end > i_begin ? (i_end - i_begin + step - 1) / step : 0;
-  const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-
-  // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
-  // and neither is looked at before the next stage's turn.  The anchor needs one row per half stage: 16
-  // tokens that start at a multiple of 16 lie in one page, one behind the other.
-  auto load_token = [&](int it) -> int {
-    const int i = i_begin + step * it + (GATHER ? lane : lane & 16);
-    if (i >= i_end) return kNoToken;
-    return GATHER ? __ldg(sel + i) : i;
-  };
-  // the first token (reuse) or page (anchor) is on its way while q is
-  int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0,
-      page_index = 0;
-  auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
-    token_1 = token_2;
-    if (GATHER && (token_1 < 0 || token_1 >= T)) {
-      bad |= i_begin + step * it + lane < i_end;
-      token_1 = kNoToken;
-    }
-    if (token_1 != kNoToken) {
-      page_index = (int)(__umulhi((uint32_t)token_1, a.page_mul) >> a.page_shift);
-      page_1 = __ldg(table + page_index);
-    }
-    token_2 = load_token(it + 1);
-  };
-  if (!GATHER) load_page(0);
-  uint32_t masks[kStages];  // rows present, stage by stage in order of use
-  auto issue = [&](int it, int st, uint32_t& mask) {
-    // in the page store; of no meaning (and so unsigned) unless the token and its page are good
-    const int place = (int)(((uint32_t)page_1 * (uint32_t)a.Hkv + (uint32_t)h) * (uint32_t)a.page_size +
-                            ((uint32_t)token_1 - (uint32_t)page_index * (uint32_t)a.page_size));
-    const bool here = token_1 != kNoToken, good = (unsigned)page_1 < (unsigned)a.num_pages;
-    bad |= here && !good;
-    const uint32_t dst = ring + (uint32_t)st * kStageBytes;
-    if constexpr (GATHER) {
-      const int row = here && good ? place : -1;
-      load_page(it + 1);
-      mask = __ballot_sync(0xffffffffu, row >= 0);
-      // 320 chunks of 16 bytes, ten to a row; the two of a 32-byte sector go to neighbouring lanes
-#pragma unroll
-      for (int i = 0; i < 10; ++i) {
-        const int u = lane + 2 * i, r = (u * 205) >> 11;  // (lane + 32 i) / 10 = r + 3 i
-        const int pl = __shfl_sync(0xffffffffu, row, r + 3 * i);
-        copy16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
-               pl >= 0 ? 16 : 0, policy);
-      }
-    } else {
-      const int rows = here && good ? min(i_end - token_1, 16) : 0;
-      load_page(it + 1);
-      mask = __ballot_sync(0xffffffffu, (lane & 15) < rows);
-      if ((lane & 15) == 0) {  // two copies, each announced by its own lane (of no bytes, where there are no rows)
-        mbar_expect_tx(bar + 8 * st, (uint32_t)rows * kQ4Row);
-        if (rows) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, (uint32_t)rows * kQ4Row,
-                            bar + 8 * st, policy);
-      }
-    }
-  };
-
-  Query<PAIR> qx;
-  load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
-  if (GATHER) load_page(0);
-  State w;
-  w.m0 = w.m1 = -INFINITY;
-  w.l0 = w.l1 = 0.f;
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    w.z[g][0] = w.z[g][1] = 0.f;
-    w.c[g][0] = w.c[g][1] = biased_pow2(kMaxC);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
-  }
-  float* lrow = a.logits + (bh * a.max_T + i_begin + (int)half + tok_a) * G + col;
-  const int64_t eight = 8 * G;  // logits of 8 tokens
-  float base0 = 0.f, base1 = 0.f;              // finite_max of the maxima
-
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (s < n_iter) issue(s, (st + s) % kStages, masks[s]);
-    if constexpr (GATHER) cp_async_commit();
-  }
-  int st_in = (st + kStages - 1) % kStages;
-  int it = 0;
-  for (; it < n_iter; ++it) {
-    if (it + kStages - 1 < n_iter) issue(it + kStages - 1, st_in, masks[kStages - 1]);
-    if (++st_in == kStages) st_in = 0;
-    if constexpr (GATHER) {
-      cp_async_commit();
-      cp_async_wait<kStages - 1>();
-      __syncwarp();
-    } else {
-      alive = __all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (uint32_t)phase, a.status));
-      if (!alive) break;
-    }
-    const uint32_t rows = ring + (uint32_t)st * kStageBytes;
-    const uint32_t mask = masks[0];
-    const bool full = mask == 0xffffffffu;
-    if (!GATHER && !full) {
-      // Rows that are not there become zeros (the reuse's copies have seen to that): whatever stands there
-      // would meet weights of 0 and columns of zeros, and 0 times a stray NaN is not 0.
-      for (int i = lane; i < (int)kStageBytes / 16; i += 32)
-        if (!((mask >> (i / 10)) & 1u)) sts128(rows + 16 * i, make_uint4(0, 0, 0, 0));
-      fence_proxy_async_smem();  // copies come to the same place later
-      __syncwarp();
-    }
-    constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
-    const uint32_t mine = rows + half * kQ4Row + row_a;
-    float s[kSets][4];
-    scores<PAIR>(qx, rows, row_a, mine, tig, s[0]);
-    if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, s[1]);
-#pragma unroll
-    for (int u = 0; u < kSets; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p20f * ((i & 1) ? qx.f1 : qx.f0);
-    if (!full) {
-#pragma unroll
-      for (int u = 0; u < 2 * kSets; ++u)
-        if (!((mask >> (8 * u + half + tok_a)) & 1u)) s[u >> 1][2 * (u & 1)] = s[u >> 1][2 * (u & 1) + 1] = -INFINITY;
-    }
     if constexpr (!GATHER) {
-      if (full && !(G & 1)) {
-        if (col < G) {
+      const int n = stages_of(T, a.max_T), end = (int)min((int64_t)at + left, (int64_t)(n + kUnitCost));
+      if (end <= max(at, kUnitCost)) return;  // nothing left, or no stage of the last unit
+      left -= end - at;
+      const int s0 = max(at - kUnitCost, 0), ns = end - kUnitCost - s0;
+      if (threadIdx.x == 0) {
+        int2* parts = a.parts + ((int64_t)b * a.Hkv + h);
+        if (s0 == 0) parts->x = (int)blockIdx.x;
+        if (s0 + ns == n) parts->y = (int)blockIdx.x;
+      }
+      i_begin = (s0 + (int)((int64_t)ns * warp / kWarps)) * kStageRows;
+      i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
+    }
+    const int64_t bh = (int64_t)b * a.Hkv + h;
+    const int n_iter = i_end > i_begin ? (i_end - i_begin + step - 1) / step : 0;
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
+
+    // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
+    // and neither is looked at before the next stage's turn.  The anchor needs one row per half stage: 16
+    // tokens that start at a multiple of 16 lie in one page, one behind the other.
+    auto load_token = [&](int it) -> int {
+      const int i = i_begin + step * it + (GATHER ? lane : lane & 16);
+      if (i >= i_end) return kNoToken;
+      return GATHER ? __ldg(sel + i) : i;
+    };
+    // the first token (reuse) or page (anchor) is on its way while q is
+    int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0,
+        page_index = 0;
+    auto load_page = [&](int it) {  // of stage it, whose tokens have been loaded; then the tokens of it + 1
+      token_1 = token_2;
+      if (GATHER && (token_1 < 0 || token_1 >= T)) {
+        bad |= i_begin + step * it + lane < i_end;
+        token_1 = kNoToken;
+      }
+      if (token_1 != kNoToken) {
+        page_index = (int)(__umulhi((uint32_t)token_1, a.page_mul) >> a.page_shift);
+        page_1 = __ldg(table + page_index);
+      }
+      token_2 = load_token(it + 1);
+    };
+    if (!GATHER) load_page(0);
+    uint32_t masks[kStages];  // rows present, stage by stage in order of use
+    auto issue = [&](int it, int st, uint32_t& mask) {
+      // in the page store; of no meaning (and so unsigned) unless the token and its page are good
+      const int place = (int)(((uint32_t)page_1 * (uint32_t)a.Hkv + (uint32_t)h) * (uint32_t)a.page_size +
+                              ((uint32_t)token_1 - (uint32_t)page_index * (uint32_t)a.page_size));
+      const bool here = token_1 != kNoToken, good = (unsigned)page_1 < (unsigned)a.num_pages;
+      bad |= here && !good;
+      const uint32_t dst = ring + (uint32_t)st * kStageBytes;
+      if constexpr (GATHER) {
+        const int row = here && good ? place : -1;
+        load_page(it + 1);
+        mask = __ballot_sync(0xffffffffu, row >= 0);
+        // 320 chunks of 16 bytes, ten to a row; the two of a 32-byte sector go to neighbouring lanes
 #pragma unroll
-          for (int u = 0; u < 2 * kSets; ++u)
-            *reinterpret_cast<float2*>(lrow + u * eight) = make_float2(s[u >> 1][2 * (u & 1)], s[u >> 1][2 * (u & 1) + 1]);
+        for (int i = 0; i < 10; ++i) {
+          const int u = lane + 2 * i, r = (u * 205) >> 11;  // (lane + 32 i) / 10 = r + 3 i
+          const int pl = __shfl_sync(0xffffffffu, row, r + 3 * i);
+          copy16(dst + 16 * lane + 512 * i, a.pages + ((int64_t)max(pl, 0) * kQ4Row + 16 * (u - 10 * r)),
+                 pl >= 0 ? 16 : 0, policy);
         }
       } else {
-        const int rest = i_end - (i_begin + kStageRows * it + (int)half + tok_a);
-#pragma unroll
-        for (int u = 0; u < 2 * kSets; ++u) {
-          if (rest > 8 * u) {
-            if (col < G) lrow[u * eight] = s[u >> 1][2 * (u & 1)];
-            if (col + 1 < G) lrow[u * eight + 1] = s[u >> 1][2 * (u & 1) + 1];
-          }
+        const int rows = here && good ? min(i_end - token_1, 16) : 0;
+        load_page(it + 1);
+        mask = __ballot_sync(0xffffffffu, (lane & 15) < rows);
+        if ((lane & 15) == 0) {  // two copies, each announced by its own lane (of no bytes, where there are no rows)
+          mbar_expect_tx(bar + 8 * st, (uint32_t)rows * kQ4Row);
+          if (rows) bulk_load(dst + (uint32_t)lane * kQ4Row, a.pages + (int64_t)place * kQ4Row, (uint32_t)rows * kQ4Row,
+                              bar + 8 * st, policy);
         }
       }
-      lrow += 4 * eight;
-    }
-    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
-    if constexpr (!PAIR) {
-      x0 = fmaxf(x0, fmaxf(s[1][0], s[1][2]));
-      x1 = fmaxf(x1, fmaxf(s[1][1], s[1][3]));
-    }
-    if (__any_sync(0xffffffffu, x0 > w.m0 + 8.f || x1 > w.m1 + 8.f)) {
-      const float n0 = fmaxf(w.m0, head_max<PAIR>(x0)), n1 = fmaxf(w.m1, head_max<PAIR>(x1));
-      base0 = finite_max(n0);
-      base1 = finite_max(n1);
-      const float al0 = fast_exp2(w.m0 - base0), al1 = fast_exp2(w.m1 - base1);
-      w.m0 = n0;
-      w.m1 = n1;
-      w.l0 *= al0;
-      w.l1 *= al1;
-      rebase(w, 0, al0);
-      rebase(w, 1, al1);
-    }
+    };
+
+    Query<PAIR> qx;
+    load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
+    if (GATHER) load_page(0);
+    State w;
+    w.m0 = w.m1 = -INFINITY;
+    w.l0 = w.l1 = 0.f;
 #pragma unroll
-    for (int u = 0; u < kSets; ++u) {
+    for (int g = 0; g < 4; ++g) {
+      w.z[g][0] = w.z[g][1] = 0.f;
+      w.c[g][0] = w.c[g][1] = biased_pow2(kMaxC);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
-      w.l0 += s[u][0] + s[u][2];
-      w.l1 += s[u][1] + s[u][3];
+      for (int i = 0; i < 4; ++i) w.o[g][0][i] = w.o[g][1][i] = 0.f;
     }
-    // A half-precision output is rounded no more coarsely than a weight: there the weights get a second term.
-    Weights b;
-    weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, tig, b);
-    values<!PAIR && F16>(w, rows, gid, tig, b);
-    __syncwarp();  // the stage is read: it may be refilled
+    float* lrow = a.logits + (bh * a.max_T + i_begin + (int)half + tok_a) * G + col;
+    const int64_t eight = 8 * G;  // logits of 8 tokens
+    float base0 = 0.f, base1 = 0.f;              // finite_max of the maxima
+
 #pragma unroll
-    for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
-    if (++st == kStages) {
-      st = 0;
-      phase ^= 1;
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (s < n_iter) issue(s, (st + s) % kStages, masks[s]);
+      if constexpr (GATHER) cp_async_commit();
     }
-  }
-  if (!alive) {  // gave up on a copy: wait, with the same bound, for the others in flight
-    for (int k = 1; k < kStages && it + k < n_iter; ++k) {
+    int st_in = (st + kStages - 1) % kStages;
+    int it = 0;
+    for (; it < n_iter; ++it) {
+      if (it + kStages - 1 < n_iter) issue(it + kStages - 1, st_in, masks[kStages - 1]);
+      if (++st_in == kStages) st_in = 0;
+      if constexpr (GATHER) {
+        cp_async_commit();
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+      } else {
+        alive = __all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (uint32_t)phase, a.status));
+        if (!alive) break;
+      }
+      const uint32_t rows = ring + (uint32_t)st * kStageBytes;
+      const uint32_t mask = masks[0];
+      const bool full = mask == 0xffffffffu;
+      if (!GATHER && !full) {
+        // Rows that are not there become zeros (the reuse's copies have seen to that): whatever stands there
+        // would meet weights of 0 and columns of zeros, and 0 times a stray NaN is not 0.
+        for (int i = lane; i < (int)kStageBytes / 16; i += 32)
+          if (!((mask >> (i / 10)) & 1u)) sts128(rows + 16 * i, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();  // copies come to the same place later
+        __syncwarp();
+      }
+      constexpr int kSets = PAIR ? 1 : 2;  // sets of 16 rows that a lane works on
+      const uint32_t mine = rows + half * kQ4Row + row_a;
+      float s[kSets][4];
+      scores<PAIR>(qx, rows, row_a, mine, tig, s[0]);
+      if constexpr (!PAIR) scores<PAIR>(qx, rows + 16 * kQ4Row, row_a, mine + 16 * kQ4Row, tig, s[1]);
+#pragma unroll
+      for (int u = 0; u < kSets; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] = s[u][i] * 0x1p20f * ((i & 1) ? qx.f1 : qx.f0);
+      if (!full) {
+#pragma unroll
+        for (int u = 0; u < 2 * kSets; ++u)
+          if (!((mask >> (8 * u + half + tok_a)) & 1u)) s[u >> 1][2 * (u & 1)] = s[u >> 1][2 * (u & 1) + 1] = -INFINITY;
+      }
+      if constexpr (!GATHER) {
+        if (full && !(G & 1)) {
+          if (col < G) {
+#pragma unroll
+            for (int u = 0; u < 2 * kSets; ++u) {
+              const float* x = &s[u >> 1][2 * (u & 1)];
+              *reinterpret_cast<float2*>(lrow + u * eight) = make_float2(x[0], x[1]);
+            }
+          }
+        } else {
+          const int rest = i_end - (i_begin + kStageRows * it + (int)half + tok_a);
+#pragma unroll
+          for (int u = 0; u < 2 * kSets; ++u) {
+            if (rest > 8 * u) {
+              if (col < G) lrow[u * eight] = s[u >> 1][2 * (u & 1)];
+              if (col + 1 < G) lrow[u * eight + 1] = s[u >> 1][2 * (u & 1) + 1];
+            }
+          }
+        }
+        lrow += 4 * eight;
+      }
+      float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
+      if constexpr (!PAIR) {
+        x0 = fmaxf(x0, fmaxf(s[1][0], s[1][2]));
+        x1 = fmaxf(x1, fmaxf(s[1][1], s[1][3]));
+      }
+      if (__any_sync(0xffffffffu, x0 > w.m0 + 8.f || x1 > w.m1 + 8.f)) {
+        const float n0 = fmaxf(w.m0, head_max<PAIR>(x0)), n1 = fmaxf(w.m1, head_max<PAIR>(x1));
+        base0 = finite_max(n0);
+        base1 = finite_max(n1);
+        const float al0 = fast_exp2(w.m0 - base0), al1 = fast_exp2(w.m1 - base1);
+        w.m0 = n0;
+        w.m1 = n1;
+        w.l0 *= al0;
+        w.l1 *= al1;
+        rebase(w, 0, al0);
+        rebase(w, 1, al1);
+      }
+#pragma unroll
+      for (int u = 0; u < kSets; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] = fast_exp2(s[u][i] - ((i & 1) ? base1 : base0));
+        w.l0 += s[u][0] + s[u][2];
+        w.l1 += s[u][1] + s[u][3];
+      }
+      // a half-precision output is rounded no more coarsely than a weight: there the weights get a second term
+      Weights wt;
+      weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, tig, wt);
+      values<!PAIR && F16>(w, rows, gid, tig, wt);
+      __syncwarp();  // the stage is read: it may be refilled
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
       if (++st == kStages) {
         st = 0;
         phase ^= 1;
       }
-      mbar_wait(bar + 8 * st, (uint32_t)phase, a.status);
     }
-  }
+    if (!alive) {  // gave up on a copy: wait, with the same bound, for the others in flight
+      for (int k = 1; k < kStages && it + k < n_iter; ++k) {
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
+        mbar_wait(bar + 8 * st, (uint32_t)phase, a.status);
+      }
+    }
 
-  if (bad) flag_status(a.status, kStatusBadIndex);
-  bad = false;
+    if (bad) flag_status(a.status, kStatusBadIndex);
+    bad = false;
 
-  // ---- merge the four warps; the rings are free once all are here ------------
-  const float l0 = head_sum<PAIR>(w.l0), l1 = head_sum<PAIR>(w.l1);
-  __syncthreads();
-  float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
-  const bool owner = !PAIR || tig < 2;
-  if constexpr (PAIR && F16) {  // columns 4..7 hold the weights' second terms
+    // ---- merge the four warps; the rings are free once all are here ------------
+    const float l0 = head_sum<PAIR>(w.l0), l1 = head_sum<PAIR>(w.l1);
+    __syncthreads();
+    float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
+    const bool owner = !PAIR || tig < 2;
+    if constexpr (PAIR && F16) {  // columns 4..7 hold the weights' second terms
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float& o = w.o[i >> 3][(i >> 2) & 1][i & 3];
-      o += __shfl_xor_sync(0xffffffffu, o, 2);
+      for (int i = 0; i < 32; ++i) {
+        float& o = w.o[i >> 3][(i >> 2) & 1][i & 3];
+        o += __shfl_xor_sync(0xffffffffu, o, 2);
+      }
     }
-  }
-  if (gid == 0 && owner) {
-    sm_m[warp][col] = w.m0;
-    sm_m[warp][col + 1] = w.m1;
-    sm_l[warp][col] = l0;
-    sm_l[warp][col + 1] = l1;
-  }
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^-24 c
-    const float z0 = head_sum<PAIR>(w.z[g][0]), z1 = head_sum<PAIR>(w.z[g][1]);
-    if (!owner) continue;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int d = 32 * g + 4 * gid + 2 * u;
-      const float* o = w.o[g][u];
-      *reinterpret_cast<float2*>(&sm_o[warp][col][d]) =
-          make_float2(fmaf((o[0] - o[2]) * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
-      *reinterpret_cast<float2*>(&sm_o[warp][col + 1][d]) =
-          make_float2(fmaf((o[1] - o[3]) * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
+    if (gid == 0 && owner) {
+      sm_m[warp][col] = w.m0;
+      sm_m[warp][col + 1] = w.m1;
+      sm_l[warp][col] = l0;
+      sm_l[warp][col + 1] = l1;
     }
-  }
-  __syncthreads();
-  const int d = threadIdx.x;  // kThreads == kHeadDim
-  for (int g = 0; g < G; ++g) {
-    float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i][g]);
+    for (int g = 0; g < 4; ++g) {
+      const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^-24 c
+      const float z0 = head_sum<PAIR>(w.z[g][0]), z1 = head_sum<PAIR>(w.z[g][1]);
+      if (!owner) continue;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float f = fast_exp2(sm_m[i][g] - finite_max(M));
-      acc += f * sm_o[i][g][d];
-      L += f * sm_l[i][g];
+      for (int u = 0; u < 2; ++u) {
+        const int d = 32 * g + 4 * gid + 2 * u;
+        const float* o = w.o[g][u];
+        *reinterpret_cast<float2*>(&sm_o[warp][col][d]) =
+            make_float2(fmaf((o[0] - o[2]) * 0x1p12f, up0, z0), fmaf(o[2] * 0x1p8f, up0, z0));
+        *reinterpret_cast<float2*>(&sm_o[warp][col + 1][d]) =
+            make_float2(fmaf((o[1] - o[3]) * 0x1p12f, up1, z1), fmaf(o[3] * 0x1p8f, up1, z1));
+      }
+    }
+    __syncthreads();
+    const int d = threadIdx.x;  // kThreads == kHeadDim
+    for (int g = 0; g < G; ++g) {
+      float M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm_m[i][g]);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float f = fast_exp2(sm_m[i][g] - finite_max(M));
+        acc += f * sm_o[i][g][d];
+        L += f * sm_l[i][g];
+      }
+      if constexpr (GATHER) {
+        sm_po[g][d] = acc;
+        if (d == 0) {
+          sm_pm[g] = M;
+          sm_pl[g] = L;
+        }
+      } else {
+        const int64_t slot = ((int64_t)blockIdx.x + bh) * G + g;
+        a.part_o[slot * kHeadDim + d] = acc;
+        if (d == 0) {
+          a.part_ml[slot * 2] = M;
+          a.part_ml[slot * 2 + 1] = L;
+        }
+      }
     }
     if constexpr (GATHER) {
-      sm_po[g][d] = acc;
-      if (d == 0) {
-        sm_pm[g] = M;
-        sm_pl[g] = L;
-      }
-    } else {
-      const int64_t slot = ((int64_t)blockIdx.x + bh) * G + g;
-      a.part_o[slot * kHeadDim + d] = acc;
-      if (d == 0) {
-        a.part_ml[slot * 2] = M;
-        a.part_ml[slot * 2 + 1] = L;
-      }
-    }
-  }
-  if constexpr (GATHER) {
-    // the splits of (b, h) are one cluster: they merge through distributed shared memory
-    namespace cg = cooperative_groups;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    const int ns = (int)cluster.num_blocks();
-    for (int g = (int)cluster.block_rank(); g < G; g += ns) {  // the blocks share the heads
-      float M = -INFINITY, L = 0.f, acc = 0.f;
+      // the splits of (b, h) are one cluster: they merge through distributed shared memory
+      namespace cg = cooperative_groups;
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      const int ns = (int)cluster.num_blocks();
+      for (int g = (int)cluster.block_rank(); g < G; g += ns) {  // the blocks share the heads
+        float M = -INFINITY, L = 0.f, acc = 0.f;
 #pragma unroll 4
-      for (int r = 0; r < ns; ++r) M = fmaxf(M, *cluster.map_shared_rank(&sm_pm[g], r));
+        for (int r = 0; r < ns; ++r) M = fmaxf(M, *cluster.map_shared_rank(&sm_pm[g], r));
 #pragma unroll 4
-      for (int r = 0; r < ns; ++r) {
-        const float f = fast_exp2(*cluster.map_shared_rank(&sm_pm[g], r) - finite_max(M));
-        L += f * *cluster.map_shared_rank(&sm_pl[g], r);
-        acc += f * *cluster.map_shared_rank(&sm_po[g][d], r);
+        for (int r = 0; r < ns; ++r) {
+          const float f = fast_exp2(*cluster.map_shared_rank(&sm_pm[g], r) - finite_max(M));
+          L += f * *cluster.map_shared_rank(&sm_pl[g], r);
+          acc += f * *cluster.map_shared_rank(&sm_po[g][d], r);
+        }
+        a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
+        if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
       }
-      a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + d] = to_bits<F16>(L == 0.f ? 0.f : acc / L);
-      if (a.lse && d == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(M, L) * kLn2;
+      cluster.sync();  // peers keep their shared memory until all have read it
+      return;
     }
-    cluster.sync();  // peers keep their shared memory until all have read it
-    return;
-  }
-  // the next unit; a warp that gave up takes its whole block along
-  fence_proxy_async_smem();  // the merge wrote where the next copies go
-  if (__syncthreads_or(!alive) || left <= 0) return;
-  at = 0;
-  if (++h == a.Hkv) {
-    h = 0;
-    do {
-      if (++b == a.B) return;
-      T = a.seq_len[b];
-    } while (stages_of(T, a.max_T) == 0);
-  }
+    // the next unit; a warp that gave up takes its whole block along
+    fence_proxy_async_smem();  // the merge wrote where the next copies go
+    if (__syncthreads_or(!alive) || left <= 0) return;
+    at = 0;
+    if (++h == a.Hkv) {
+      h = 0;
+      do {
+        if (++b == a.B) return;
+        T = a.seq_len[b];
+      } while (stages_of(T, a.max_T) == 0);
+    }
   }
 }
 
@@ -942,7 +949,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
       const int t = t0 + i * kCombineThreads + threadIdx.x;
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        x[i][j] = t < t_hi ? reinterpret_cast<const float4*>(lrow)[(int64_t)t * V + j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[i][j] = t < t_hi ? reinterpret_cast<const float4*>(lrow)[(int64_t)t * V + j]
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   if (V > 0 && !merge) load((int)t_lo);
@@ -993,7 +1001,8 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
       for (int i = 0; i < kCombineThreads / 32; ++i) o += reinterpret_cast<const float*>(s_o[i])[threadIdx.x];
       a.out[((int64_t)b * a.Hq + h * G + g) * kHeadDim + threadIdx.x] = to_bits<F16>(s_L[g] == 0.f ? 0.f : o / s_L[g]);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(s_L[g] == 0.f ? -INFINITY : s_M[g], s_L[g]) * kLn2;
+    if (a.lse && threadIdx.x == 0)
+      a.lse[(int64_t)b * a.Hq + h * G + g] = lse2_of(s_L[g] == 0.f ? -INFINITY : s_M[g], s_L[g]) * kLn2;
     return;
   }
   float* prow = a.pooled + bh * a.ld_pooled;

@@ -176,20 +176,27 @@ struct Query {
   float f0, f1;                    // factors of heads 2 tig, 2 tig + 1 to base-2 logits (times 2^20)
 };
 
+// The lane's query words: 8 channels of each scale group, of head gid (PAIR: gid & 3).
+template <bool PAIR>
+__device__ __forceinline__ void fetch_query(uint4 (&w)[4], const uint16_t* q, int G, int gid, int tig) {
+  const int head = PAIR ? gid & 3 : gid;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    // columns past the last head are padding: load a valid row and zero it
+    w[g] = ldg16(q + (head < G ? head : G - 1) * kHeadDim + 32 * g + 8 * tig);
+    if (head >= G) w[g] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <bool PAIR, bool F16>
-__device__ __forceinline__ void load_query(Query<PAIR>& x, const uint16_t* q, int G, float scale_log2, int gid,
-                                           int tig) {
+__device__ __forceinline__ void build_query(Query<PAIR>& x, const uint4 (&w)[4], float scale_log2, int gid, int tig) {
   float v[4][8];
   float top = 0.f;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    // columns past the last head are padding: load a valid row and zero it
-    const int head = PAIR ? gid & 3 : gid;
-    uint4 w = ldg16(q + (head < G ? head : G - 1) * kHeadDim + 32 * g + 8 * tig);
-    if (head >= G) w = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      unpack2<F16>(word_of(w, i), v[g][2 * i], v[g][2 * i + 1]);
+      unpack2<F16>(word_of(w[g], i), v[g][2 * i], v[g][2 * i + 1]);
       top = fmaxf(top, fmaxf(fabsf(v[g][2 * i]), fabsf(v[g][2 * i + 1])));
     }
   }
@@ -676,9 +683,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       }
     };
 
-    Query<PAIR> qx;
-    load_query<PAIR, F16>(qx, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, a.scale_log2, gid, tig);
+    uint4 query[4];
+    fetch_query<PAIR>(query, a.q + ((int64_t)b * a.Hq + (int64_t)h * G) * kHeadDim, G, gid, tig);
     if (GATHER) load_page(0);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (s < n_iter) issue(s, (st + s) % kStages, masks[s]);
+      if constexpr (GATHER) cp_async_commit();
+    }
+    Query<PAIR> qx;
+    build_query<PAIR, F16>(qx, query, a.scale_log2, gid, tig);
     State w;
     w.m0 = w.m1 = -INFINITY;
     w.l0 = w.l1 = 0.f;
@@ -691,13 +705,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
     float* lrow = a.logits + (bh * a.max_T + i_begin + (int)half + tok_a) * G + col;
     const int64_t eight = 8 * G;  // logits of 8 tokens
-    float base0 = 0.f, base1 = 0.f;              // finite_max of the maxima
+    float base0 = 0.f, base1 = 0.f;  // finite_max of the maxima
 
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (s < n_iter) issue(s, (st + s) % kStages, masks[s]);
-      if constexpr (GATHER) cp_async_commit();
-    }
     int st_in = (st + kStages - 1) % kStages;
     int it = 0;
     for (; it < n_iter; ++it) {

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .binding import Q4_ROW_BYTES, Shape, Strides, check
+from .binding import Q4_ROW_BYTES, Shape, check
 
 HEAD_DIM = 128
 TILE = 128
@@ -277,25 +277,25 @@ def _rows(name: str, t, dtype: torch.dtype, shape: tuple, dev: int):
     return t.data_ptr(), t.stride()
 
 
-# A decode step makes some of these calls for every layer: what a call does not have to build anew
-# on the host (structures of its sizes, by value) is not.
+# A decode step makes some of these calls for every layer, so their host side is kept short: each
+# tensor is looked at once, and the entry point is called through _hostcall.
 _shape = functools.lru_cache(maxsize=256)(Shape)
-_strides = functools.lru_cache(maxsize=1024)(Strides)
 
 
-def _call(dev: int, name: str, *args) -> None:
-    """The entry point on the current stream of the tensors' device, which need
-    not be the current device."""
-    fn = getattr(_lib(), name)
+def _call(dev: int, name: str, sfx: str, *args) -> None:
+    """An entry point of binding.HOSTCALLS on the current stream of the tensors' device,
+    which need not be the current device."""
+    fn = getattr(_lib(), "host_" + name)
+    f16 = 1 if sfx else 0
     if dev < 0:
-        rc = fn(*args, _stream())
+        rc = fn(f16, *args, _stream())
     elif dev == torch._C._cuda_getDevice():  # the tensors' checks have seen to it that CUDA is up
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        rc = fn(f16, *args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            rc = fn(f16, *args, torch._C._cuda_getCurrentRawStream(dev))
     if rc:
-        check(rc, name)
+        check(rc, binding.HOSTCALLS[name] + sfx)
 
 
 def _end(a: int, n0: int, n1: int, n2: int, st) -> int:
@@ -351,9 +351,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
         ins = (qp, _end(qp, B, N, Hq, qs), qs, Hq), (kp, _end(kp, B, N, Hkv, ks), ks, Hkv)
         _need_apart("q_out", qop, _end(qop, B, Hq, N, qos), qos, Hq, ins)
         _need_apart("k_out", kop, _end(kop, B, Hkv, N, kos), kos, Hkv, ins)
-    _call(dev, "kascade_qk_norm_rope" + sfx, _shape(B, Hq, Hkv, d), N, qp, _strides(*qs[:3]), kp, _strides(*ks[:3]),
-          pos, inv, qw, kw, float(eps), 1 if interleaved else 0, qop, _strides(qos[0], qos[2], qos[1]),
-          kop, _strides(kos[0], kos[2], kos[1]))
+    _call(dev, "norm_rope", sfx, B, Hq, Hkv, d, N, qp, qs[0], qs[1], qs[2], kp, ks[0], ks[1], ks[2], pos, inv, qw, kw, eps,
+          1 if interleaved else 0, qop, qos[0], qos[2], qos[1], kop, kos[0], kos[2], kos[1])
     return q_out, k_out
 
 
@@ -388,9 +387,8 @@ def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     first = _sized("start", start, torch.int32, B, dev)
     n = None if count is None else _sized("count", count, torch.int32, B, dev)
-    _call(dev, "kascade_kv_write_paged_q4" + sfx, _shape(B, Hkv, Hkv, d), N, k.data_ptr(),
-          _strides(ks[0], ks[2], ks[1]), vp, _strides(vs[0], vs[2], vs[1]), pages, num_pages, table, max_pages,
-          int(page_size), first, n)
+    _call(dev, "kv_write", sfx, B, Hkv, Hkv, d, N, k.data_ptr(), ks[0], ks[2], ks[1], vp, vs[0], vs[2], vs[1], pages,
+          num_pages, table, max_pages, page_size, first, n)
     return kv_pages
 
 
@@ -415,8 +413,7 @@ def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int
     kp, vp = _sized("k", k, dtype, size, dev), _sized("v", v, dtype, size, dev)
     if abs(kp - vp) < 2 * size:
         raise ValueError("k and v share memory")
-    _call(dev, "kascade_kv_read_paged_q4" + sfx, _shape(B, Hkv, Hkv, HEAD_DIM), int(N), pages, num_pages, table, max_pages,
-          int(page_size), first, n, kp, vp)
+    _call(dev, "kv_read", sfx, B, Hkv, Hkv, HEAD_DIM, N, pages, num_pages, table, max_pages, page_size, first, n, kp, vp)
     return k, v
 
 
@@ -443,15 +440,14 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     op = _sized("out", out, dt, B * Hq * d, dev)
     lp = _sized("lse", lse, torch.float32, B * Hq, dev)
     pp = _sized("pooled", pooled, torch.float32, B * Hkv * ld_pooled, dev)
-    shape = _shape(B, Hq, Hkv, d)
     if ws is None:
-        ws_bytes = max(16, _lib().kascade_decode_anchor_paged_q4_workspace_bytes(shape, max_T))
+        ws_bytes = max(16, _lib().kascade_decode_anchor_paged_q4_workspace_bytes(_shape(B, Hq, Hkv, d), max_T))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     else:
         ws_bytes = _ws_bytes(ws)
         _need_device("ws", ws, dev)
-    _call(dev, "kascade_decode_anchor_paged_q4" + sfx, shape, q.data_ptr(), pages, num_pages, table, max_pages,
-          int(page_size), lens, int(max_T), float(scale), op, lp, pp, int(ld_pooled), ws.data_ptr(), ws_bytes)
+    _call(dev, "decode_anchor", sfx, B, Hq, Hkv, d, q.data_ptr(), pages, num_pages, table, max_pages, page_size, lens,
+          max_T, scale, op, lp, pp, ld_pooled, ws.data_ptr(), ws_bytes)
     return out, lse, pooled
 
 
@@ -474,8 +470,8 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
     op = _sized("out", out, dt, B * Hq * d, dev)
     lp = _sized("lse", lse, torch.float32, B * Hq, dev)
-    _call(dev, "kascade_decode_reuse_paged_q4" + sfx, _shape(B, Hq, Hkv, d), q.data_ptr(), pages, num_pages, table,
-          max_pages, int(page_size), lens, ip, np, k_max, mp, float(scale), op, lp)
+    _call(dev, "decode_reuse", sfx, B, Hq, Hkv, d, q.data_ptr(), pages, num_pages, table, max_pages, page_size, lens, ip,
+          np, k_max, mp, scale, op, lp)
     return out, lse
 
 

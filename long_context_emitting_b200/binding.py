@@ -149,6 +149,28 @@ for _name in ("kascade_decode_anchor", "kascade_decode_reuse", "kascade_prefill_
 _lib = None
 
 
+# What _hostcall calls, in its order: host_<name> of the library object takes the entry point's
+# arguments as plain numbers (half precision 0 or 1 first, structures by their fields).
+HOSTCALLS = {
+    "norm_rope": "kascade_qk_norm_rope",
+    "kv_write": "kascade_kv_write_paged_q4",
+    "kv_read": "kascade_kv_read_paged_q4",
+    "decode_anchor": "kascade_decode_anchor_paged_q4",
+    "decode_reuse": "kascade_decode_reuse_paged_q4",
+}
+
+
+def _bind_hostcalls(lib: ctypes.CDLL) -> None:
+    try:
+        from . import _hostcall
+    except ImportError as e:
+        raise RuntimeError("_hostcall.so is missing: build it with `python -m long_context_emitting_b200.build`") from e
+    _hostcall.bind(*(ctypes.cast(getattr(lib, name + sfx), ctypes.c_void_p).value
+                     for name in HOSTCALLS.values() for sfx in ("", "_f16")))
+    for name in HOSTCALLS:
+        setattr(lib, "host_" + name, getattr(_hostcall, name))
+
+
 def load() -> ctypes.CDLL:
     """Load libkascade.so (built in-tree) and declare every signature."""
     global _lib
@@ -162,6 +184,7 @@ def load() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    _bind_hostcalls(lib)
     _lib = lib
     return lib
 

@@ -8,12 +8,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkascade.so")
+HOSTCALL = os.path.join(HERE, "_hostcall.so")  # CPython module: calls of the decode step's small entry points
 SOURCES = ["api.cu", "decode.cu", "topk.cu", "prefill.cu", "noalloc.cu", "calib.cu", "selftest.cu",
            "norm_rope.cu", "cache_q4.cu", "decode_q4.cu"]
 HEADERS = ["common.cuh", "internal.h", "tcgen05.cuh", "exp2_poly.cuh", "f32x2.cuh", "q4.cuh"]
@@ -33,14 +35,15 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, h) for h in HEADERS if os.path.exists(os.path.join(CSRC, h))]
+    files.append(os.path.join(CSRC, "hostcall.c"))
     files.append(os.path.join(ROOT, "include", "kascade.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOSTCALL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOSTCALL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -69,6 +72,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static"])
     os.replace(tmp, LIB)
+    tmp = HOSTCALL + ".tmp"
+    subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
+                           os.path.join(CSRC, "hostcall.c"), "-o", tmp])
+    os.replace(tmp, HOSTCALL)
     return LIB
 
 

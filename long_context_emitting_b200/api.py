@@ -333,9 +333,10 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     dt = q.dtype
     sfx = _data_suffix(q, k)
     Hkv = k.shape[2]
-    _need_rows("q", q, dt, (B, N, Hq, d))
     dev = q.get_device()
-    qp, qs = q.data_ptr(), q.stride()
+    if dev < 0:
+        _need_rows("q", q, dt, (B, N, Hq, d))
+    qp, qs = _rows("q", q, dt, (B, N, Hq, d), dev)
     kp, ks = _rows("k", k, dt, (B, N, Hkv, d), dev)
     pos = _sized("positions", positions, torch.int32, B * N, dev)
     inv = _sized("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
@@ -348,9 +349,12 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     qop, qos = _rows("q_out", q_out, dt, (B, Hq, N, d), dev)
     kop, kos = _rows("k_out", k_out, dt, (B, Hkv, N, d), dev)
     if B and N:
-        ins = (qp, _end(qp, B, N, Hq, qs), qs, Hq), (kp, _end(kp, B, N, Hkv, ks), ks, Hkv)
-        _need_apart("q_out", qop, _end(qop, B, Hq, N, qos), qos, Hq, ins)
-        _need_apart("k_out", kop, _end(kop, B, Hkv, N, kos), kos, Hkv, ins)
+        qe, ke = _end(qp, B, N, Hq, qs), _end(kp, B, N, Hkv, ks)
+        first, last = min(qp, kp), max(qe, ke)  # most outputs lie outside of all that
+        if qop < last and (end := _end(qop, B, Hq, N, qos)) > first:
+            _need_apart("q_out", qop, end, qos, Hq, ((qp, qe, qs, Hq), (kp, ke, ks, Hkv)))
+        if kop < last and (end := _end(kop, B, Hkv, N, kos)) > first:
+            _need_apart("k_out", kop, end, kos, Hkv, ((qp, qe, qs, Hq), (kp, ke, ks, Hkv)))
     _call(dev, "norm_rope", sfx, B, Hq, Hkv, d, N, qp, qs[0], qs[1], qs[2], kp, ks[0], ks[1], ks[2], pos, inv, qw, kw, eps,
           1 if interleaved else 0, qop, qos[0], qos[2], qos[1], kop, kos[0], kos[2], kos[1])
     return q_out, k_out
@@ -380,14 +384,16 @@ def kv_write_paged_q4(k, v, kv_pages, block_table, page_size: int, start, count=
     """
     B, Hkv, N, d = k.shape
     sfx = _data_suffix(k, v)
-    _need_rows("k", k, k.dtype, (B, Hkv, N, d))
+    dt, shape = k.dtype, (B, Hkv, N, d)
     dev = k.get_device()
-    ks = k.stride()
-    vp, vs = _rows("v", v, k.dtype, (B, Hkv, N, d), dev)
+    if dev < 0:
+        _need_rows("k", k, dt, shape)
+    kp, ks = _rows("k", k, dt, shape, dev)
+    vp, vs = _rows("v", v, dt, shape, dev)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     first = _sized("start", start, torch.int32, B, dev)
     n = None if count is None else _sized("count", count, torch.int32, B, dev)
-    _call(dev, "kv_write", sfx, B, Hkv, Hkv, d, N, k.data_ptr(), ks[0], ks[2], ks[1], vp, vs[0], vs[2], vs[1], pages,
+    _call(dev, "kv_write", sfx, B, Hkv, Hkv, d, N, kp, ks[0], ks[2], ks[1], vp, vs[0], vs[2], vs[1], pages,
           num_pages, table, max_pages, page_size, first, n)
     return kv_pages
 
@@ -399,11 +405,12 @@ def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int
     are left as they were.  ``count`` None reads N tokens of every sequence."""
     B = start.numel()
     Hkv = kv_pages.shape[1]
-    sfx = "_f16" if dtype == torch.float16 else ""
+    sfx = "_f16" if dtype is torch.float16 else ""
     if dtype not in _DATA_DTYPES:
         raise TypeError("dtype must be bfloat16 or float16")
-    _need_cuda("kv_pages", kv_pages, torch.uint8)
     dev = kv_pages.get_device()
+    if dev < 0:
+        _need_cuda("kv_pages", kv_pages, torch.uint8)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     first = _sized("start", start, torch.int32, B, dev)
     n = None if count is None else _sized("count", count, torch.int32, B, dev)
@@ -428,8 +435,10 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     B, Hq, d = q.shape
     sfx = _data_suffix(q)
     dt = q.dtype
-    _need_cuda("q", q, dt)
     dev = q.get_device()
+    if dev < 0:
+        _need_cuda("q", q, dt)
+    qp = _sized("q", q, dt, 0, dev)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     lens = _sized("seq_len", seq_len, torch.int32, B, dev)
     if ld_pooled is None:
@@ -446,7 +455,7 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     else:
         ws_bytes = _ws_bytes(ws)
         _need_device("ws", ws, dev)
-    _call(dev, "decode_anchor", sfx, B, Hq, Hkv, d, q.data_ptr(), pages, num_pages, table, max_pages, page_size, lens,
+    _call(dev, "decode_anchor", sfx, B, Hq, Hkv, d, qp, pages, num_pages, table, max_pages, page_size, lens,
           max_T, scale, op, lp, pp, ld_pooled, ws.data_ptr(), ws_bytes)
     return out, lse, pooled
 
@@ -458,8 +467,10 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     B, Hq, d = q.shape
     sfx = _data_suffix(q)
     dt = q.dtype
-    _need_cuda("q", q, dt)
     dev = q.get_device()
+    if dev < 0:
+        _need_cuda("q", q, dt)
+    qp = _sized("q", q, dt, 0, dev)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     k_max = idx.shape[-1]
     lens = _sized("seq_len", seq_len, torch.int32, B, dev)
@@ -470,7 +481,7 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
     op = _sized("out", out, dt, B * Hq * d, dev)
     lp = _sized("lse", lse, torch.float32, B * Hq, dev)
-    _call(dev, "decode_reuse", sfx, B, Hq, Hkv, d, q.data_ptr(), pages, num_pages, table, max_pages, page_size, lens, ip,
+    _call(dev, "decode_reuse", sfx, B, Hq, Hkv, d, qp, pages, num_pages, table, max_pages, page_size, lens, ip,
           np, k_max, mp, scale, op, lp)
     return out, lse
 

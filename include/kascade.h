@@ -295,8 +295,9 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
  *   q_out, k_out  like q and k with their own strides, at least 128 where the dimension
  *            is longer than 1: strides {Hq*N*128, 128, N*128} give the [B, Hq, N, 128] that
  *            the prefill calls read, and with N = 1 the [B, Hq, 128] of the decode calls.
- *            An output may be its own input (same pointer and strides); other overlap is
- *            not allowed.
+ *            An output may be its own input (same pointer and strides); other overlap, with
+ *            the other input, with the other output or of an output's own rows, is not
+ *            allowed, and the caller sees to that.
  * Any Hq and Hkv (at most 4096) is taken here; B·N <= 2^30. */
 typedef struct {
   int64_t b, n, h; /* element strides between sequences, tokens, heads */

@@ -303,17 +303,62 @@ def _end(a: int, n0: int, n1: int, n2: int, st) -> int:
     return a + 2 * ((n0 - 1) * st[0] + (n1 - 1) * st[1] + (n2 - 1) * st[2] + HEAD_DIM)
 
 
-def _need_apart(name: str, a: int, b: int, st, H: int, ins) -> None:
-    """An output [B, H, N, 128] at bytes a to b is one of the inputs [B, N, H, 128] exactly,
-    or shares no memory with any."""
-    overlaps = False
-    for lo, hi, s, heads in ins:
-        if lo < b and a < hi:
-            if lo == a and heads == H and (s[0], s[2], s[1]) == st[:3]:
-                return
-            overlaps = True
-    if overlaps:
-        raise ValueError(f"{name} overlaps an input without being the same view")
+@functools.lru_cache(maxsize=256)
+def _rows_distinct(strides: tuple, lengths: tuple) -> bool:
+    """Whether the rows of a view lie one outside the other."""
+    extent = HEAD_DIM
+    for s, n in sorted(zip(strides, lengths)):
+        if n > 1:
+            if s < extent:
+                return False
+            extent += (n - 1) * s
+    return True
+
+
+@functools.lru_cache(maxsize=256)
+def _rows_apart(delta: int, xs: tuple, ys: tuple) -> bool:
+    """Whether two views of 16-bit rows share no byte.  The first one starts ``delta`` bytes after
+    the second; xs and ys are their (stride, length) pairs.  Looks for indices whose rows meet, the
+    longest strides first; where those are too many to look through, the answer is no."""
+    steps = []  # (bytes, least, greatest) of what an index adds to the distance
+    for (s, n), (t, m) in zip(xs, ys):
+        steps += [(2 * s, 1 - m, n - 1)] if s == t else [(2 * s, 0, n - 1), (2 * t, 1 - m, 0)]
+    steps = sorted((x for x in steps if x[0] and x[1] < x[2]), reverse=True)
+    row = 2 * HEAD_DIM
+    todo, seen = [(0, delta)], 0
+    while todo:
+        i, at = todo.pop()
+        if i == len(steps):
+            if -row < at < row:
+                return False
+            continue
+        size, a, b = steps[i]
+        least = sum(x[0] * x[1] for x in steps[i + 1:])
+        greatest = sum(x[0] * x[2] for x in steps[i + 1:])
+        a = max(a, (-row - at - greatest) // size + 1)
+        b = min(b, -((at + least - row) // size) - 1)
+        seen += max(0, b - a + 1)
+        if seen > 4096:
+            return False
+        todo += [(i + 1, at + c * size) for c in range(a, b + 1)]
+    return True
+
+
+def _need_free_outputs(B: int, N: int, views) -> None:
+    """Of q, k, q_out and k_out (name, address, heads, strides): the outputs may each be its own
+    input's view, and share no memory otherwise: not with the inputs, not with each other, and no
+    two rows of one."""
+    for name, _, H, st in views[2:]:
+        if not _rows_distinct(st, (B, N, H)):
+            raise ValueError(f"rows of {name} overlap each other")
+    v = [(name, a, _end(a, B, N, H, st), tuple([(s if n > 1 else 0, n) for s, n in zip(st, (B, N, H))]))
+         for name, a, H, st in views]
+    for x, y in ((2, 0), (2, 1), (3, 0), (3, 1), (2, 3)):
+        nx, a, a_end, xs = v[x]
+        ny, b, b_end, ys = v[y]
+        own = x - y == 2
+        if a < b_end and b < a_end and not (own and a == b and xs == ys) and not _rows_apart(a - b, xs, ys):
+            raise ValueError(f"{nx} overlaps {ny}" + (" without being the same view" if own else ""))
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -327,7 +372,9 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     rotates channels (2i, 2i+1) instead of (i, i + 64).  Returns q [B, Hq, N, 128]
     and k [B, Hkv, N, 128], the layout of the prefill calls (and, with N = 1,
     of the decode calls); outputs of that shape with any strides may be given,
-    also the inputs themselves (``q_out=q.transpose(1, 2)``).
+    also the inputs themselves (``q_out=q.transpose(1, 2)``, ``k_out`` likewise
+    over k).  Other than that the outputs share no memory with the inputs or
+    with each other.
     """
     B, N, Hq, d = q.shape
     dt = q.dtype
@@ -342,19 +389,21 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     inv = _sized("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
     qw = None if q_weight is None else _sized("q_weight", q_weight, dt, d, dev)
     kw = None if k_weight is None else _sized("k_weight", k_weight, dt, d, dev)
+    given = q_out is not None or k_out is not None
     if q_out is None:
         q_out = torch.empty(B, Hq, N, d, dtype=dt, device=q.device)
     if k_out is None:
         k_out = torch.empty(B, Hkv, N, d, dtype=dt, device=q.device)
     qop, qos = _rows("q_out", q_out, dt, (B, Hq, N, d), dev)
     kop, kos = _rows("k_out", k_out, dt, (B, Hkv, N, d), dev)
-    if B and N:
-        qe, ke = _end(qp, B, N, Hq, qs), _end(kp, B, N, Hkv, ks)
-        first, last = min(qp, kp), max(qe, ke)  # most outputs lie outside of all that
-        if qop < last and (end := _end(qop, B, Hq, N, qos)) > first:
-            _need_apart("q_out", qop, end, qos, Hq, ((qp, qe, qs, Hq), (kp, ke, ks, Hkv)))
-        if kop < last and (end := _end(kop, B, Hkv, N, kos)) > first:
-            _need_apart("k_out", kop, end, kos, Hkv, ((qp, qe, qs, Hq), (kp, ke, ks, Hkv)))
+    if given and B and N:
+        qe, ke, size = _end(qp, B, N, Hq, qs), _end(kp, B, N, Hkv, ks), 2 * B * N * d
+        first, last, qoe, koe = min(qp, kp), max(qe, ke), qop + size * Hq, kop + size * Hkv
+        # Most outputs are contiguous and lie outside of all that.
+        if not (q_out.is_contiguous() and k_out.is_contiguous() and (qop >= last or qoe <= first)
+                and (kop >= last or koe <= first) and (qoe <= kop or koe <= qop)):
+            _need_free_outputs(B, N, (("q", qp, Hq, qs), ("k", kp, Hkv, ks), ("q_out", qop, Hq, (qos[0], qos[2], qos[1])),
+                                      ("k_out", kop, Hkv, (kos[0], kos[2], kos[1]))))
     _call(dev, "norm_rope", sfx, B, Hq, Hkv, d, N, qp, qs[0], qs[1], qs[2], kp, ks[0], ks[1], ks[2], pos, inv, qw, kw, eps,
           1 if interleaved else 0, qop, qos[0], qos[2], qos[1], kop, kos[0], kos[2], kos[1])
     return q_out, k_out

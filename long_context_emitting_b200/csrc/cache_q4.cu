@@ -184,7 +184,7 @@ struct Place {
     }
     if (n >= count) return -1;
     const int t = start + n, pi = t / a.page_size;
-    const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + pi);
+    const int page = a.block_table[(int64_t)b * a.max_pages + pi];
     if (page < 0 || page >= a.num_pages) {
       if (first) flag_status(a.status, kStatusBadIndex);
       return -1;
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheArg
   bool bad = false;
   uint4 ck = make_uint4(0, 0, 0, 0), cv = ck;
   if (p.row >= 0 && p.h < p.h_end) {
-    ck = ldg16(k);
-    cv = ldg16(v);
+    ck = load16(k);
+    cv = load16(v);
   }
   const int passes = (p.h_end - (int)blockIdx.y * a.heads_per_block + kStep - 1) / kStep;  // of the block
   for (int i = 0, h = p.h; i < passes; ++i, h += kStep) {
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 4) cache_write_kernel(const CacheArg
     k += (int64_t)kStep * a.ks.h;
     v += (int64_t)kStep * a.vs.h;
     if (p.row >= 0 && h + kStep < p.h_end) {
-      nk = ldg16(k);
-      nv = ldg16(v);
+      nk = load16(k);
+      nv = load16(v);
     }
     // even lanes work out K's scale of their group, odd lanes V's
     const uint32_t ek = group_ends<F16>(ck), ev = group_ends<F16>(cv);
@@ -286,9 +286,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheArgs a)
   const uint8_t* src = a.pages + (p.row + (int64_t)p.h * a.page_size) * kQ4Row;
   uint32_t kw = 0, vw = 0, tail = 0;
   auto load = [&](uint32_t& k, uint32_t& v, uint32_t& t) {
-    k = __ldg(reinterpret_cast<const uint32_t*>(src) + 4 * j + g);
-    v = __ldg(reinterpret_cast<const uint32_t*>(src + kQ4V) + 2 * (2 * j + (int)odd) + (g >> 1));
-    t = __ldg(reinterpret_cast<const uint16_t*>(src + kQ4Tail) + l);
+    k = reinterpret_cast<const uint32_t*>(src)[4 * j + g];
+    v = reinterpret_cast<const uint32_t*>(src + kQ4V)[2 * (2 * j + (int)odd) + (g >> 1)];
+    t = reinterpret_cast<const uint16_t*>(src + kQ4Tail)[l];
   };
   if (p.row >= 0 && p.h < p.h_end) load(kw, vw, tail);
   const int base = threadIdx.x & 16;

@@ -84,6 +84,13 @@ __device__ __forceinline__ uint4 ldg16(const void* p) {
   return r;
 }
 
+// 16 bytes by an ordinary load.  A kernel that is launched early (grid_dependency_wait) may be resident
+// while kernels two or three places ahead of it still run: allow_dependents_launch() at a kernel's start
+// lets in its successor, and that one the next.  What those write changes during this kernel's lifetime,
+// so it may not be read through the non-coherent path (ld.global.nc, __ldg), which wants it constant for
+// all of that time; such a kernel keeps that path for what no kernel writes (weights).
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int w) {
   return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
 }

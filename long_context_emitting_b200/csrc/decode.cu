@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_gather_kernel(const SplitA
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int gq = gid < G ? gid : G - 1;
-    uint4 t = ldg16(a.q + ((int64_t)b * a.Hq + h * G + gq) * kHeadDim + 8 * (tig + 4 * j));
+    uint4 t = load16(a.q + ((int64_t)b * a.Hq + h * G + gq) * kHeadDim + 8 * (tig + 4 * j));
     if (gid >= G) t = make_uint4(0, 0, 0, 0);
     qf[j][0] = t.x; qf[j][1] = t.y; qf[j][2] = t.z; qf[j][3] = t.w;
   }

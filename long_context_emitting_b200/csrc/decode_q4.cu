@@ -183,7 +183,7 @@ __device__ __forceinline__ void fetch_query(uint4 (&w)[4], const uint16_t* q, in
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     // columns past the last head are padding: load a valid row and zero it
-    w[g] = ldg16(q + (head < G ? head : G - 1) * kHeadDim + 32 * g + 8 * tig);
+    w[g] = load16(q + (head < G ? head : G - 1) * kHeadDim + 32 * g + 8 * tig);
     if (head >= G) w[g] = make_uint4(0, 0, 0, 0);
   }
 }
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     i_begin = ((int)blockIdx.x * kWarps + warp) * kStageRows;
     i_end = n_items;
     // the first indices do not wait for the row's length
-    token_0 = i_begin + lane < a.k_max ? __ldg(sel + i_begin + lane) : 0;
+    token_0 = i_begin + lane < a.k_max ? sel[i_begin + lane] : 0;
   } else {
     const int mine = lane < a.B ? a.seq_len[lane] : 0;
     const int64_t total = line_length(a.seq_len, a.B, a.max_T, mine) * a.Hkv;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     auto load_token = [&](int it) -> int {
       const int i = i_begin + step * it + (GATHER ? lane : lane & 16);
       if (i >= i_end) return kNoToken;
-      return GATHER ? __ldg(sel + i) : i;
+      return GATHER ? sel[i] : i;
     };
     // the first token (reuse) or page (anchor) is on its way while q is
     int token_2 = !GATHER ? load_token(0) : i_begin + lane < i_end ? token_0 : kNoToken, token_1 = kNoToken, page_1 = 0,
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       }
       if (token_1 != kNoToken) {
         page_index = (int)(__umulhi((uint32_t)token_1, a.page_mul) >> a.page_shift);
-        page_1 = __ldg(table + page_index);
+        page_1 = table[page_index];
       }
       token_2 = load_token(it + 1);
     };

@@ -45,9 +45,6 @@ struct RopeArgs {
   int heads_per_block;
 };
 
-// An output may be its input's own view, so these are ordinary loads, not read-only ones.
-__device__ __forceinline__ uint4 load_row(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
 // TOK tokens x kRows / TOK heads at a time.
 template <int TOK, bool F16, bool INTER>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
@@ -90,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     }
     int h = first + row / TOK;
     const uint16_t* x0 = x + (int64_t)min(h, end - 1) * xs.h;
-    uint4 c0 = load_row(x0), c1 = load_row(x0 + 64);
+    uint4 c0 = load16(x0), c1 = load16(x0 + 64);
     for (int hh = first; hh < end; hh += kStep, h += kStep) {
       float v[16];
 #pragma unroll
@@ -100,8 +97,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
       }
       if (hh + kStep < end) {
         const uint16_t* x1 = x + (int64_t)min(h + kStep, end - 1) * xs.h;
-        c0 = load_row(x1);
-        c1 = load_row(x1 + 64);
+        c0 = load16(x1);
+        c1 = load16(x1 + 64);
       }
       if (norm) {
         float ss = 0.f;

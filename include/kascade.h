@@ -478,8 +478,10 @@ int kascade_select_anchors(const double* S, int32_t L, int32_t M, int32_t* ancho
  * current device.  The result is KASCADE_OK or one recorded code, chosen in this
  * order: KASCADE_ERR_TIMEOUT, then KASCADE_ERR_BAD_INDEX, then
  * KASCADE_ERR_NONFINITE.  It is KASCADE_ERR_CUDA if the wait fails.
- * KASCADE_ERR_TIMEOUT means that a prefill kernel's bounded wait gave up after
- * about 2 s; that call's outputs are incomplete, and the context stays usable. */
+ * KASCADE_ERR_TIMEOUT means that a bounded wait of a prefill kernel or of the 4-bit
+ * decode anchor gave up after about 2 s; that call's outputs are incomplete (the
+ * anchor's are NaN for every sequence and key head whose tokens were not all read),
+ * and the context stays usable. */
 int kascade_get_device_status(void* stream);
 
 /* Diagnostic for the failure path above.  Launches one CTA on `stream`.  Its
@@ -492,6 +494,17 @@ int kascade_get_device_status(void* stream);
  * KASCADE_ERR_CUDA if the launch fails.  No memory is read or written apart from
  * the status word. */
 int kascade_selftest_wait_timeout(int32_t spin, void* stream);
+
+/* Diagnostic for what the 4-bit decode anchor does after such a wait: the call
+ * kascade_decode_anchor_paged_q4 with the same arguments, in which one thread block
+ * of its first kernel, number `block` (>= 0; none if there are fewer), behaves as if
+ * its first wait had given up.  It records the timeout bit, reads no tokens and ends
+ * as usual; results of the units that it had a part of are NaN, the others complete. */
+int kascade_selftest_anchor_q4_gives_up(int32_t block, kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                        int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                                        int32_t page_size, const int32_t* seq_len, int32_t max_T, float scale,
+                                        uint16_t* out, float* lse, float* pooled, int64_t ld_pooled, void* ws,
+                                        size_t ws_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kascade_status_string(int status);

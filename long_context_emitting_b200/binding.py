@@ -69,6 +69,7 @@ EXPORTS = (
     "kascade_get_device_status",
     "kascade_status_string",
     "kascade_selftest_wait_timeout",
+    "kascade_selftest_anchor_q4_gives_up",
 )
 
 
@@ -138,6 +139,8 @@ _SIGNATURES = {
     "kascade_get_device_status": (ctypes.c_int, [_P]),
     "kascade_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kascade_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_int32, _P]),
+    "kascade_selftest_anchor_q4_gives_up": (ctypes.c_int, [_I32, Shape, _P, _P, _I32, _P, _I32, _I32, _P, _I32, _F, _P,
+                                                           _P, _P, _I64, _P, _SZ, _P]),
 }
 # fp16 variants take the same arguments as their bfloat16 counterparts
 for _name in ("kascade_decode_anchor", "kascade_decode_reuse", "kascade_prefill_anchor",

@@ -499,7 +499,7 @@ static int decode_anchor_paged_q4_impl(kascade_shape s, const uint16_t* q, const
                                        const int32_t* block_table, int32_t max_pages, int32_t page_size,
                                        const int32_t* seq_len, int32_t max_T, float scale, uint16_t* out, float* lse,
                                        float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream,
-                                       bool f16) {
+                                       bool f16, int give_up = -1) {
   int rc = check_shape(s);
   if (rc) return rc;
   if (max_T < 0 || ld_pooled < max_T || (ld_pooled & 3) || !std::isfinite(scale)) return KASCADE_ERR_INVALID_ARG;
@@ -520,6 +520,7 @@ static int decode_anchor_paged_q4_impl(kascade_shape s, const uint16_t* q, const
   p.seq_len = seq_len; p.max_T = max_T;
   p.scale = scale; p.out = out; p.lse = lse; p.pooled = pooled; p.ld_pooled = ld_pooled;
   p.ws = ws;
+  p.give_up = give_up;
   p.status = device_status_ptr();
   if (!p.status) return KASCADE_ERR_CUDA;
   return from_cuda(launch_decode_anchor_q4(p, static_cast<cudaStream_t>(stream)));
@@ -539,6 +540,16 @@ int kascade_decode_anchor_paged_q4_f16(kascade_shape s, const uint16_t* q, const
                                        float* pooled, int64_t ld_pooled, void* ws, size_t ws_bytes, void* stream) {
   return decode_anchor_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, max_T,
                                      scale, out, lse, pooled, ld_pooled, ws, ws_bytes, stream, true);
+}
+
+int kascade_selftest_anchor_q4_gives_up(int32_t block, kascade_shape s, const uint16_t* q, const uint8_t* kv_pages,
+                                        int32_t num_pages, const int32_t* block_table, int32_t max_pages,
+                                        int32_t page_size, const int32_t* seq_len, int32_t max_T, float scale,
+                                        uint16_t* out, float* lse, float* pooled, int64_t ld_pooled, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  if (block < 0) return KASCADE_ERR_INVALID_ARG;
+  return decode_anchor_paged_q4_impl(s, q, kv_pages, num_pages, block_table, max_pages, page_size, seq_len, max_T,
+                                     scale, out, lse, pooled, ld_pooled, ws, ws_bytes, stream, false, block);
 }
 
 static int decode_reuse_paged_q4_impl(kascade_shape s, const uint16_t* q, const uint8_t* kv_pages, int32_t num_pages,

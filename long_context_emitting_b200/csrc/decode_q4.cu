@@ -53,6 +53,7 @@
 #include "tcgen05.cuh"
 
 #include <cooperative_groups.h>
+#include <math_constants.h>
 
 #include <algorithm>
 #include <cmath>
@@ -87,6 +88,7 @@ struct Q4Args {
   int k_max;
   int Hq, Hkv, G, max_T;
   int B;
+  int give_up;     // anchor: the block that gives up before its first copy (self-test), or -1
   float scale_log2;
   float* logits;   // anchor: [B, Hkv, max_T, G] base-2 scaled logits
   int2* parts;     // [B*Hkv]: first and last block of a unit
@@ -607,7 +609,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
   const int col = PAIR ? 2 * (tig & 1) : 2 * tig;  // the lane's first head
   const uint64_t policy = read_once_policy();
   int st = 0, phase = 0;
-  bool alive = true, bad = false;  // bad: an index or page out of range was met
+  bool bad = false;  // an index or page out of range was met
+  // A block whose wait for a copy gave up copies no more, but goes on along its share: each part that it
+  // owes has the sum NaN, which the second kernel hands to all results of that unit.  (Without that they
+  // would be made of an earlier call's parts, as far as the workspace holds some.)
+  bool alive = GATHER || (int)blockIdx.x != a.give_up;
 
   while (true) {
     if constexpr (!GATHER) {
@@ -619,12 +625,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
         int2* parts = a.parts + ((int64_t)b * a.Hkv + h);
         if (s0 == 0) parts->x = (int)blockIdx.x;
         if (s0 + ns == n) parts->y = (int)blockIdx.x;
+        if (!alive) flag_status(a.status, kStatusTimeout);
       }
       i_begin = (s0 + (int)((int64_t)ns * warp / kWarps)) * kStageRows;
       i_end = min((s0 + (int)((int64_t)ns * (warp + 1) / kWarps)) * kStageRows, T);
     }
     const int64_t bh = (int64_t)b * a.Hkv + h;
-    const int n_iter = i_end > i_begin ? (i_end - i_begin + step - 1) / step : 0;
+    const int n_iter = alive && i_end > i_begin ? (i_end - i_begin + step - 1) / step : 0;
     const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
 
     // Row addresses run ahead of the copies: the selected token is loaded two stages early, its page one,
@@ -817,7 +824,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
 
     // ---- merge the four warps; the rings are free once all are here ------------
     const float l0 = head_sum<PAIR>(w.l0), l1 = head_sum<PAIR>(w.l1);
-    __syncthreads();
+    if constexpr (GATHER) __syncthreads();
+    else alive = __syncthreads_and(alive);
     float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
     const bool owner = !PAIR || tig < 2;
     if constexpr (PAIR && F16) {  // columns 4..7 hold the weights' second terms
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
         a.part_o[slot * kHeadDim + d] = acc;
         if (d == 0) {
           a.part_ml[slot * 2] = M;
-          a.part_ml[slot * 2 + 1] = L;
+          a.part_ml[slot * 2 + 1] = alive ? L : CUDART_NAN_F;
         }
       }
     }
@@ -897,9 +905,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
       cluster.sync();  // peers keep their shared memory until all have read it
       return;
     }
-    // the next unit; a warp that gave up takes its whole block along
+    // the next unit
     fence_proxy_async_smem();  // the merge wrote where the next copies go
-    if (__syncthreads_or(!alive) || left <= 0) return;
+    __syncthreads();
+    if (left <= 0) return;
     at = 0;
     if (++h == a.Hkv) {
       h = 0;
@@ -966,7 +975,9 @@ __global__ void __launch_bounds__(kCombineThreads) decode_q4_combine_kernel(cons
   // the slots of this unit: those of the blocks that hold its first stage to its last
   int c0 = 0, ns = 0;
   if (T > 0) {
-    if (part.x >= 0 && part.x <= part.y && part.y < a.blocks) {  // not so if the first kernel gave up
+    // the first kernel has written both for every unit with tokens; the bounds are for lengths that
+    // someone changes between the two kernels
+    if (part.x >= 0 && part.x <= part.y && part.y < a.blocks) {
       c0 = part.x;
       ns = part.y - part.x + 1;
     }
@@ -1091,6 +1102,7 @@ Q4Args common_args(const DecodeQ4Params& p) {
   a.B = p.B; a.Hq = p.Hq; a.Hkv = p.Hkv; a.G = p.G; a.max_T = p.max_T;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.out = p.out; a.lse = p.lse; a.status = p.status;
+  a.give_up = p.give_up;
   return a;
 }
 

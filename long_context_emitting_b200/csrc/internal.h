@@ -109,6 +109,7 @@ struct DecodeQ4Params {
   int64_t ld_pooled;
   void* ws;
   unsigned* status;
+  int give_up = -1;  // anchor: see kascade_selftest_anchor_q4_gives_up
 };
 size_t decode_q4_workspace_bytes(int B, int Hkv, int G, int max_T);
 cudaError_t launch_decode_anchor_q4(const DecodeQ4Params& p, cudaStream_t st);

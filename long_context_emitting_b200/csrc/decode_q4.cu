@@ -9,29 +9,30 @@
 //   q · K_t    = sum_g [ ks_{t,g} (q_g · n_{t,g}) + km_{t,g} sum(q_g) ]
 //   out_d      = sum_t (p_t vs_{t,g}) n_{t,d}  +  sum_t p_t vm_{t,g}      (d in group g)
 // and mma.sync multiplies the codes n themselves: a nibble in bits 4..7 of a half
-// word is the half-precision subnormal n · 2^-20, exact.  (tcgen05 would want the
-// codes unpacked into shared or tensor memory first: 512 bytes written and read
-// again per row of 160.)  The other operand carries the powers of two: q (scaled
-// per head so that its largest element is near 2^14; a bfloat16 or half q is then
-// exact in half precision down to 2^-28 of that) and p · vs (below).
+// word (K) or in bits 6..9 (V) is the half-precision subnormal n · 2^-20 or n · 2^-18,
+// exact.  (tcgen05 would want the codes unpacked into shared or tensor memory first:
+// 512 bytes written and read again per row of 160.)  The other operand carries the
+// powers of two: q (scaled per head so that its largest element is near 2^14; a
+// bfloat16 or half q is then exact in half precision down to 2^-28 of that) and
+// p · vs (below).
 //   * S^T[16 tokens x 8 heads]: two m16n8k16 per scale group, whose fp32 sums
 //     the row's scales weight; the minima come in by one more mma, bfloat16
 //     minima against sum(q_g) split into three bfloat16 terms (24 bits).
-//   * O^T[128 channels x 8 heads]: per group the weights p · vs in half precision
-//     are the B operand: at most 2^-11 of each weight is lost, which against a
-//     bfloat16 output's 2^-8 does not show; for a half-precision output what is
-//     lost is a second operand.  Weights of different tokens may differ by any
-//     power of two, so each head and group has its own factor c, a power of two:
-//     the first weights, and any that would pass 2^15, are put near 2^8, where
-//     weights 2^22 times smaller still keep all their bits.  When the running
-//     maximum moves, c takes up the change and the sums stay.  The minima are
-//     summed in fp32 (8 sums per lane).
+//   * O^T[128 channels x 8 heads]: per group the weights p · vs are the B operand,
+//     in two half-precision terms (22 bits).  One alone left outputs 4e-4 off before
+//     their own rounding, which shows (bfloat16, 16 x 32K: 1.71e-3 from 64 bits
+//     instead of 1.67e-3); the second costs 5% there (147 to 154.6 us) and 14% with
+//     8 heads.  Weights of different tokens may differ by any power of two, so each
+//     head and group has its own factor c, a power of two: the first weights, and any
+//     that would pass 2^15, are put near 2^8, where weights 2^22 times smaller still
+//     keep 11 bits.  When the running maximum moves, c takes up the change and the
+//     sums stay.  The minima are summed in fp32 (8 sums per lane).
 //   * The running maximum moves only when a score exceeds it by 8 (weights then
 //     reach 2^8 instead of 1), so most stages need one vote instead of a
 //     reduction and a rescale of the sums.  Values up to 2^100 are safe from
 //     overflow on the way.
 //   * Up to 4 heads fill half the columns.  The other half then serves the second
-//     16 rows of a stage (scores) or the weights' second terms (half precision).
+//     16 rows of a stage (scores) or the weights' second terms (values).
 //
 // What bounds it, on one B200 (16 sequences of 32K, 32 heads on 8, bfloat16): the
 // first kernel reads 671 MB in 136 to 145 us (by box), 4.6 to 4.9 TB/s; loads and
@@ -347,17 +348,17 @@ __device__ __forceinline__ void rebase(State& w, int h, float al) {
   }
 }
 
-// A stage's weights as the B operands of the value products: b[block of 16 rows][group], and with
-// LOW what their rounding to half precision left.  With PAIR that stands in the columns that have no
-// head (second[] is not used): columns 0..3 of block 0 hold the weights and 4..7 the rest, of block 1
-// the other way round; the merge adds the two.
+// A stage's weights as the B operands of the value products, [block of 16 rows][group]: rounded to half
+// precision, and what that rounding left.  With PAIR the latter stands in the columns that have no head
+// (second[] is not used): columns 0..3 of block 0 hold the weights and 4..7 the rest, of block 1 the
+// other way round; the merge adds the two.
 struct Weights {
   uint32_t first[2][4][2], second[2][4][2];
 };
 
 // p: exponentials of the lane's rows a and b (layout of scores), of each set of rows.  `tail` is the
 // address of the first row a's V scales.  Also adds the minima's sums.
-template <bool PAIR, bool LOW>
+template <bool PAIR>
 __device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p)[PAIR ? 1 : 2][4], int tig,
                                         Weights& out) {
   constexpr int kSets = PAIR ? 1 : 2;
@@ -376,10 +377,8 @@ __device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p
       w1 *= f;
       const uint32_t h = pack_f16x2(w0, w1);
       hi[u >> 1][g][u & 1] = h;
-      if constexpr (LOW) {
-        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        lo[u >> 1][g][u & 1] = pack_f16x2(w0 - back.x, w1 - back.y);
-      }
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      lo[u >> 1][g][u & 1] = pack_f16x2(w0 - back.x, w1 - back.y);
     }
   };
 #pragma unroll
@@ -421,19 +420,15 @@ __device__ __forceinline__ void weights(State& w, uint32_t tail, const float (&p
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if constexpr (PAIR && LOW) {
+      if constexpr (PAIR) {
         const uint32_t other = __shfl_xor_sync(0xffffffffu, lo[0][g][i], 2);
         out.first[0][g][i] = movmatrix_trans(tig < 2 ? hi[0][g][i] : other);
         out.first[1][g][i] = movmatrix_trans(tig < 2 ? other : hi[0][g][i]);
-      } else if constexpr (PAIR) {
-        // the second rows' weights stand in columns 4..7: swap them to 0..3 (4..7 of the sums are not used)
-        out.first[0][g][i] = movmatrix_trans(hi[0][g][i]);
-        out.first[1][g][i] = __shfl_xor_sync(0xffffffffu, out.first[0][g][i], 16);
       } else {
 #pragma unroll
         for (int u = 0; u < kSets; ++u) {
           out.first[u][g][i] = movmatrix_trans(hi[u][g][i]);
-          if constexpr (LOW) out.second[u][g][i] = movmatrix_trans(lo[u][g][i]);
+          out.second[u][g][i] = movmatrix_trans(lo[u][g][i]);
         }
       }
     }
@@ -447,8 +442,11 @@ __device__ __forceinline__ void add2(float& x, float& y, float dx, float dy) {
 // O += V P for the 32 rows at `rows`.  The products of a stage start from zero and are added to the
 // sums in fp32: the matrix unit cuts each product off at the last bit of the sum that it joins, always
 // toward zero, and 2000 products of one sign would be 2^-15 short, which the minima, summed apart,
-// would not be (at 128K tokens 0.5% of the output).
-template <bool SECOND>
+// would not be (at 128K tokens 0.5% of the output).  Codes stand two bits higher than the bytes they are
+// taken from, in bits 6..9 of a half word: the unit lines products up by the operands' exponents, so every
+// bit in front of a subnormal code is one less for its products.  In bits 4..7 outputs were 7e-5 off
+// before their rounding (2.17e-4 instead of 2.10e-4 in half precision), now 2e-5; 159 instead of 154.6 us.
+template <bool PAIR>
 __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig, const Weights& b) {
   uint2 e[2][4];
 #pragma unroll
@@ -463,6 +461,7 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
   }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
+    constexpr uint32_t kHigh = 0x03c003c0u;        // high nibbles of the shifted bytes
     const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;  // half g % 2 of both rows' words
     float d[2][4];
 #pragma unroll
@@ -470,8 +469,8 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
       // whole bytes, and their high nibbles: the merge takes the difference of the two sums
       const uint32_t x = __byte_perm(g < 2 ? e[u][0].x : e[u][0].y, g < 2 ? e[u][1].x : e[u][1].y, sel);
       const uint32_t y = __byte_perm(g < 2 ? e[u][2].x : e[u][2].y, g < 2 ? e[u][3].x : e[u][3].y, sel);
-      const uint32_t a0 = x & 0x00ff00ffu, a1 = x & 0x00f000f0u, a2 = y & 0x00ff00ffu, a3 = y & 0x00f000f0u;
-      const uint32_t b0 = upper_bytes(x), b1 = b0 & 0x00f000f0u, b2 = upper_bytes(y), b3 = b2 & 0x00f000f0u;
+      const uint32_t a0 = (x & 0x00ff00ffu) << 2, a1 = a0 & kHigh, a2 = (y & 0x00ff00ffu) << 2, a3 = a2 & kHigh;
+      const uint32_t b0 = upper_bytes(x) << 2, b1 = b0 & kHigh, b2 = upper_bytes(y) << 2, b3 = b2 & kHigh;
       if (u == 0) {
         mma_f16_first(d[0], a0, a1, a2, a3, b.first[u][g][0], b.first[u][g][1]);
         mma_f16_first(d[1], b0, b1, b2, b3, b.first[u][g][0], b.first[u][g][1]);
@@ -479,7 +478,7 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
         mma_f16_16816(d[0], a0, a1, a2, a3, b.first[u][g][0], b.first[u][g][1]);
         mma_f16_16816(d[1], b0, b1, b2, b3, b.first[u][g][0], b.first[u][g][1]);
       }
-      if constexpr (SECOND) {
+      if constexpr (!PAIR) {
         mma_f16_16816(d[0], a0, a1, a2, a3, b.second[u][g][0], b.second[u][g][1]);
         mma_f16_16816(d[1], b0, b1, b2, b3, b.second[u][g][0], b.second[u][g][1]);
       }
@@ -797,10 +796,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
         w.l0 += s[u][0] + s[u][2];
         w.l1 += s[u][1] + s[u][3];
       }
-      // a half-precision output is rounded no more coarsely than a weight: there the weights get a second term
       Weights wt;
-      weights<PAIR, F16>(w, mine + kQ4Tail + 16, s, tig, wt);
-      values<!PAIR && F16>(w, rows, gid, tig, wt);
+      weights<PAIR>(w, mine + kQ4Tail + 16, s, tig, wt);
+      values<PAIR>(w, rows, gid, tig, wt);
       __syncwarp();  // the stage is read: it may be refilled
 #pragma unroll
       for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
@@ -828,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     else alive = __syncthreads_and(alive);
     float (*sm_o)[8][kHeadDim] = reinterpret_cast<float (*)[8][kHeadDim]>(smem);
     const bool owner = !PAIR || tig < 2;
-    if constexpr (PAIR && F16) {  // columns 4..7 hold the weights' second terms
+    if constexpr (PAIR) {  // columns 4..7 hold the weights' second terms
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         float& o = w.o[i >> 3][(i >> 2) & 1][i & 3];
@@ -843,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const Q
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float up0 = 0x1p12f / w.c[g][0], up1 = 0x1p12f / w.c[g][1];  // sums are in 2^-24 c
+      const float up0 = 0x1p10f / w.c[g][0], up1 = 0x1p10f / w.c[g][1];  // sums are in 2^-22 c
       const float z0 = head_sum<PAIR>(w.z[g][0]), z1 = head_sum<PAIR>(w.z[g][1]);
       if (!owner) continue;
 #pragma unroll

@@ -2,7 +2,7 @@
  * convention: plain numbers in, a status out.  Through ctypes the same call costs
  * 2.1 to 2.5 us of argument conversion, more than the launch itself; here it is a
  * few tenths of one.  The addresses come from the loaded libkascade.so (bind), so
- * this module links to nothing of it. */
+ * this module links to nothing of it; a call before that raises. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -34,11 +34,15 @@ static int numbers(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, Py_ssiz
 #define PTR(type, i) ((type*)(intptr_t)v[i])
 #define STRIDES(i) ((kascade_strides){v[i], v[(i) + 1], v[(i) + 2]})
 #define SHAPE(i) ((kascade_shape){(int32_t)v[i], (int32_t)v[(i) + 1], (int32_t)v[(i) + 2], (int32_t)v[(i) + 3]})
-#define CALL(expr)             \
-  int rc;                      \
-  Py_BEGIN_ALLOW_THREADS;      \
-  rc = (expr);                 \
-  Py_END_ALLOW_THREADS;        \
+#define CALL(expr)                                                               \
+  int rc;                                                                        \
+  if (!fn) {                                                                     \
+    PyErr_SetString(PyExc_RuntimeError, "no addresses yet: bind() comes first"); \
+    return NULL;                                                                 \
+  }                                                                              \
+  Py_BEGIN_ALLOW_THREADS;                                                        \
+  rc = (expr);                                                                   \
+  Py_END_ALLOW_THREADS;                                                          \
   return PyLong_FromLong(rc)
 
 /* f16, B, Hq, Hkv, d, N, q, 3 strides, k, 3 strides, positions, inv_freq, q_weight, k_weight, eps,

@@ -7,6 +7,7 @@ fails loudly when the library has not been built: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -153,7 +154,8 @@ _lib = None
 
 
 # What _hostcall calls, in its order: host_<name> of the library object takes the entry point's
-# arguments as plain numbers (half precision 0 or 1 first, structures by their fields).
+# arguments as plain numbers (half precision 0 or 1 first, structures by their fields).  Where that
+# module has not been built (it needs Python's headers), the same calls go through ctypes.
 HOSTCALLS = {
     "norm_rope": "kascade_qk_norm_rope",
     "kv_write": "kascade_kv_write_paged_q4",
@@ -163,11 +165,40 @@ HOSTCALLS = {
 }
 
 
+def ctypes_hostcall(lib: ctypes.CDLL, name: str):
+    """host_<name> through ctypes: the same arguments, refusals and status, 2 us slower."""
+    fns = [getattr(lib, HOSTCALLS[name] + sfx) for sfx in ("", "_f16")]
+    types = _SIGNATURES[HOSTCALLS[name]][1]
+    plain = [f for t in types for f in ([x for _, x in t._fields_] if issubclass(t, ctypes.Structure) else [t])]
+
+    def number(t, x):
+        if t is _F:
+            return float(x)
+        x = None if x is None else operator.index(x)
+        if x is None:
+            return x if t is _P else 0
+        bits = 8 * ctypes.sizeof(_I32 if t is _I32 else _I64)
+        if not -(1 << bits - 1) <= x < 1 << bits - 1:
+            raise OverflowError(f"{x} does not fit {bits} bits")
+        return x
+
+    def call(*args):
+        if len(args) != 1 + len(plain):
+            raise TypeError(f"{len(args)} arguments, not {1 + len(plain)}")
+        half = number(_I32, args[0])
+        given = iter([number(t, x) for t, x in zip(plain, args[1:])])
+        return fns[half != 0](*[t(*[next(given) for _ in t._fields_]) if issubclass(t, ctypes.Structure) else next(given)
+                                for t in types])
+    return call
+
+
 def _bind_hostcalls(lib: ctypes.CDLL) -> None:
     try:
         from . import _hostcall
-    except ImportError as e:
-        raise RuntimeError("_hostcall.so is missing: build it with `python -m long_context_emitting_b200.build`") from e
+    except ImportError:
+        for name in HOSTCALLS:
+            setattr(lib, "host_" + name, ctypes_hostcall(lib, name))
+        return
     _hostcall.bind(*(ctypes.cast(getattr(lib, name + sfx), ctypes.c_void_p).value
                      for name in HOSTCALLS.values() for sfx in ("", "_f16")))
     for name in HOSTCALLS:

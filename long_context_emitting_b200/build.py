@@ -15,7 +15,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkascade.so")
-HOSTCALL = os.path.join(HERE, "_hostcall.so")  # CPython module: calls of the decode step's small entry points
+# CPython module: calls of the decode step's small entry points.  Its name carries the interpreter's
+# tag, so that another Python of the same checkout neither imports it nor takes it for its own.
+HOSTCALL = os.path.join(HERE, "_hostcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "decode.cu", "topk.cu", "prefill.cu", "noalloc.cu", "calib.cu", "selftest.cu",
            "norm_rope.cu", "cache_q4.cu", "decode_q4.cu"]
 HEADERS = ["common.cuh", "internal.h", "tcgen05.cuh", "exp2_poly.cuh", "f32x2.cuh", "q4.cuh"]
@@ -40,11 +42,24 @@ def _inputs():
     return files
 
 
+def python_headers() -> str | None:
+    """Where Python.h is, or None: without it the library goes without its CPython module."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) else None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOSTCALL):
+    made = [LIB, HOSTCALL] if python_headers() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(HOSTCALL))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def hostcall_command(out: str) -> list:
+    """nvcc, which hands C files to the host compiler that it uses anyway."""
+    return [nvcc(), *ARCH, "-O2", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-Wall", f"-I{python_headers()}",
+            os.path.join(CSRC, "hostcall.c"), "-o", out]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -72,10 +87,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static"])
     os.replace(tmp, LIB)
-    tmp = HOSTCALL + ".tmp"
-    subprocess.check_call(["gcc", "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
-                           os.path.join(CSRC, "hostcall.c"), "-o", tmp])
-    os.replace(tmp, HOSTCALL)
+    untagged = os.path.join(HERE, "_hostcall.so")  # of earlier builds: any interpreter would import it
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    if python_headers():
+        tmp = HOSTCALL + ".tmp"
+        subprocess.check_call(hostcall_command(tmp))
+        os.replace(tmp, HOSTCALL)
+    else:
+        sys.stderr.write("no Python.h: built without _hostcall, its calls go through ctypes (2 us each)\n")
     return LIB
 
 

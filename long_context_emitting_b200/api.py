@@ -257,13 +257,33 @@ def _need_device(name: str, t: torch.Tensor, dev: int) -> None:
         raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
 
 
-def _sized(name: str, t, dtype: torch.dtype, n: int, dev: int) -> int:
-    """The address of a tensor that passes _need_size and is on device ``dev``."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.numel() >= n
+def _whole(name: str, t, dtype: torch.dtype, dev: int) -> int:
+    """The address of a contiguous tensor on device ``dev``, whatever its size."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _need_cuda(name, t, dtype)
+        _need_device(name, t, dev)
+    return t.data_ptr()
+
+
+def _sized(name: str, t, dtype: torch.dtype, n: int, dev: int, inner: tuple = ()) -> int:
+    """The address of a tensor on device ``dev`` whose first ``n`` elements are what the call wants: a
+    contiguous one of that size, or a longer one whose dimensions after the first are ``inner``
+    (buffers for more sequences), so that its rows lie where the call looks for them."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.numel() == n
             and t.is_contiguous()):
         _need_size(name, t, dtype, n)
         _need_device(name, t, dev)
+        if t.numel() > n and t.dim() > 1 and tuple(t.shape[1:]) != inner:
+            raise ValueError(f"{name} is {list(t.shape)}; a longer buffer than {n} elements must be {['...', *inner]}")
     return t.data_ptr()
+
+
+def _exactly(name: str, t, dtype: torch.dtype, n: int, dev: int) -> int:
+    """The address of a contiguous tensor of ``n`` elements on device ``dev``."""
+    p = _sized(name, t, dtype, n, dev)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    return p
 
 
 def _rows(name: str, t, dtype: torch.dtype, shape: tuple, dev: int):
@@ -385,10 +405,12 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
         _need_rows("q", q, dt, (B, N, Hq, d))
     qp, qs = _rows("q", q, dt, (B, N, Hq, d), dev)
     kp, ks = _rows("k", k, dt, (B, N, Hkv, d), dev)
-    pos = _sized("positions", positions, torch.int32, B * N, dev)
-    inv = _sized("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
-    qw = None if q_weight is None else _sized("q_weight", q_weight, dt, d, dev)
-    kw = None if k_weight is None else _sized("k_weight", k_weight, dt, d, dev)
+    pos = _sized("positions", positions, torch.int32, B * N, dev, (N,))
+    if N > 1 and positions.dim() > 1 and positions.shape[-1] != N:
+        raise ValueError(f"positions must be [{B}, {N}], got {list(positions.shape)}")
+    inv = _exactly("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
+    qw = None if q_weight is None else _exactly("q_weight", q_weight, dt, d, dev)
+    kw = None if k_weight is None else _exactly("k_weight", k_weight, dt, d, dev)
     given = q_out is not None or k_out is not None
     if q_out is None:
         q_out = torch.empty(B, Hq, N, d, dtype=dt, device=q.device)
@@ -413,8 +435,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
 def _pages_q4(kv_pages, block_table, B: int, Hkv: int, page_size: int, dev: int):
     """Address and number of pages of a store [num_pages, Hkv, page_size, 160], address and row
     length of a block table with a row of page numbers for each of the B sequences."""
-    pages = _sized("kv_pages", kv_pages, torch.uint8, 0, dev)
-    table = _sized("block_table", block_table, torch.int32, 0, dev)
+    pages = _whole("kv_pages", kv_pages, torch.uint8, dev)
+    table = _whole("block_table", block_table, torch.int32, dev)
     shape, rows = kv_pages.shape, block_table.shape
     if len(shape) != 4 or shape[1:] != (Hkv, page_size, Q4_ROW_BYTES):
         raise ValueError(f"kv_pages must be [num_pages, {Hkv}, {page_size}, {Q4_ROW_BYTES}], got {tuple(shape)}")
@@ -466,7 +488,8 @@ def kv_read_paged_q4(kv_pages, block_table, page_size: int, start, count, N: int
     k = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if k is None else k
     v = torch.empty(B, Hkv, N, HEAD_DIM, dtype=dtype, device=kv_pages.device) if v is None else v
     size = B * Hkv * N * HEAD_DIM
-    kp, vp = _sized("k", k, dtype, size, dev), _sized("v", v, dtype, size, dev)
+    inner = (Hkv, N, HEAD_DIM)
+    kp, vp = _sized("k", k, dtype, size, dev, inner), _sized("v", v, dtype, size, dev, inner)
     if abs(kp - vp) < 2 * size:
         raise ValueError("k and v share memory")
     _call(dev, "kv_read", sfx, B, Hkv, Hkv, HEAD_DIM, N, pages, num_pages, table, max_pages, page_size, first, n, kp, vp)
@@ -487,7 +510,7 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     dev = q.get_device()
     if dev < 0:
         _need_cuda("q", q, dt)
-    qp = _sized("q", q, dt, 0, dev)
+    qp = _whole("q", q, dt, dev)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     lens = _sized("seq_len", seq_len, torch.int32, B, dev)
     if ld_pooled is None:
@@ -495,9 +518,9 @@ def decode_anchor_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, ma
     out = torch.empty(B, Hq, d, dtype=dt, device=q.device) if out is None else out
     lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
     pooled = torch.empty(B, Hkv, ld_pooled, dtype=torch.float32, device=q.device) if pooled is None else pooled
-    op = _sized("out", out, dt, B * Hq * d, dev)
-    lp = _sized("lse", lse, torch.float32, B * Hq, dev)
-    pp = _sized("pooled", pooled, torch.float32, B * Hkv * ld_pooled, dev)
+    op = _sized("out", out, dt, B * Hq * d, dev, (Hq, d))
+    lp = _sized("lse", lse, torch.float32, B * Hq, dev, (Hq,))
+    pp = _sized("pooled", pooled, torch.float32, B * Hkv * ld_pooled, dev, (Hkv, ld_pooled))
     if ws is None:
         ws_bytes = max(16, _lib().kascade_decode_anchor_paged_q4_workspace_bytes(_shape(B, Hq, Hkv, d), max_T))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
@@ -519,17 +542,17 @@ def decode_reuse_paged_q4(q, kv_pages, block_table, page_size: int, seq_len, idx
     dev = q.get_device()
     if dev < 0:
         _need_cuda("q", q, dt)
-    qp = _sized("q", q, dt, 0, dev)
+    qp = _whole("q", q, dt, dev)
     pages, num_pages, table, max_pages = _pages_q4(kv_pages, block_table, B, Hkv, page_size, dev)
     k_max = idx.shape[-1]
     lens = _sized("seq_len", seq_len, torch.int32, B, dev)
-    ip = _sized("idx", idx, torch.int32, B * Hkv * k_max, dev)
-    np = _sized("idx_k", idx_k, torch.int32, B * Hkv, dev)
+    ip = _sized("idx", idx, torch.int32, B * Hkv * k_max, dev, (Hkv, k_max))
+    np = _sized("idx_k", idx_k, torch.int32, B * Hkv, dev, (Hkv,))
     mp = _sized("head_map", head_map, torch.int32, Hkv, dev)
     out = torch.empty(B, Hq, d, dtype=dt, device=q.device) if out is None else out
     lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if lse is None else lse
-    op = _sized("out", out, dt, B * Hq * d, dev)
-    lp = _sized("lse", lse, torch.float32, B * Hq, dev)
+    op = _sized("out", out, dt, B * Hq * d, dev, (Hq, d))
+    lp = _sized("lse", lse, torch.float32, B * Hq, dev, (Hq,))
     _call(dev, "decode_reuse", sfx, B, Hq, Hkv, d, qp, pages, num_pages, table, max_pages, page_size, lens, ip,
           np, k_max, mp, scale, op, lp)
     return out, lse

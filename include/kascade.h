@@ -286,8 +286,8 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
  * the rest in fp32, and a row is rounded once, when it is stored.
  *
  *   q        bf16, logical [B, N, Hq, 128]: element strides q_strides between sequences,
- *            tokens and heads (multiples of 8, not negative); the channels of a row are
- *            adjacent.  k likewise with Hkv heads.  Views into a packed projection
+ *            tokens and heads (multiples of 8, not negative; of no meaning where that
+ *            dimension is 1 long); the channels of a row are adjacent.  k likewise with Hkv heads.  Views into a packed projection
  *            output are the usual case.
  *   positions int32 [B, N] (any value); inv_freq fp32 [64]
  *   q_weight, k_weight  bf16 [128] or NULL each

@@ -347,13 +347,15 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
 }
 
 // ------------------------------------------- head norms and rotation --
-// Strides of a [B, N, H, 128] view: 16-byte rows, no negative step.
-static bool strides_ok(const kascade_strides& t) {
-  return t.b >= 0 && t.n >= 0 && t.h >= 0 && !((t.b | t.n | t.h) & 7);
+// Strides of a [B, N, H, 128] view: 16-byte rows, no negative step.  Where a dimension is 1 long its
+// stride is of no meaning (PyTorch leaves any number there) and is never used but times 0.
+static bool stride_ok(int64_t stride, int length) { return length == 1 || (stride >= 0 && !(stride & 7)); }
+static bool strides_ok(const kascade_strides& t, int B, int N, int H) {
+  return stride_ok(t.b, B) && stride_ok(t.n, N) && stride_ok(t.h, H);
 }
 // The same for a view that is written: rows of different (b, n, h) must not be one row.
 static bool out_strides_ok(const kascade_strides& t, int B, int N, int H) {
-  return strides_ok(t) && (B == 1 || t.b >= kHeadDim) && (N == 1 || t.n >= kHeadDim) && (H == 1 || t.h >= kHeadDim);
+  return strides_ok(t, B, N, H) && (B == 1 || t.b >= kHeadDim) && (N == 1 || t.n >= kHeadDim) && (H == 1 || t.h >= kHeadDim);
 }
 
 static int qk_norm_rope_impl(kascade_shape s, int32_t N, const uint16_t* q, kascade_strides q_strides,
@@ -370,7 +372,7 @@ static int qk_norm_rope_impl(kascade_shape s, int32_t N, const uint16_t* q, kasc
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
       !aligned16(k_weight) || ((uintptr_t)positions & 3) || ((uintptr_t)inv_freq & 3))
     return KASCADE_ERR_INVALID_ARG;
-  if (!strides_ok(q_strides) || !strides_ok(k_strides) || !out_strides_ok(q_out_strides, s.B, N, s.Hq) ||
+  if (!strides_ok(q_strides, s.B, N, s.Hq) || !strides_ok(k_strides, s.B, N, s.Hkv) || !out_strides_ok(q_out_strides, s.B, N, s.Hq) ||
       !out_strides_ok(k_out_strides, s.B, N, s.Hkv))
     return KASCADE_ERR_INVALID_ARG;
   NormRopeParams p = {};
@@ -426,7 +428,7 @@ static int kv_write_paged_q4_impl(kascade_shape s, int32_t N, const uint16_t* k,
   if (rc || s.B == 0 || N == 0) return rc;
   if ((rc = check_pages_q4(kv_pages, block_table, num_pages, max_pages, page_size, s.Hkv))) return rc;
   if (!k || !v || !start || !aligned16(k) || !aligned16(v) || ((uintptr_t)start & 3) || ((uintptr_t)count & 3) ||
-      !strides_ok(k_strides) || !strides_ok(v_strides))
+      !strides_ok(k_strides, s.B, N, s.Hkv) || !strides_ok(v_strides, s.B, N, s.Hkv))
     return KASCADE_ERR_INVALID_ARG;
   CacheQ4Params p = {};
   p.B = s.B; p.N = N; p.Hkv = s.Hkv; p.f16 = f16;

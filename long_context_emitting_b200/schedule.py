@@ -31,6 +31,8 @@ def anchor_for_layer(anchors: Sequence[int], layer: int) -> int:
 class DecodeSchedule:
     """One decode step (one new token per sequence) through ``n_layers`` layers."""
 
+    ROW_BYTES = api.HEAD_DIM * 2 * 2   # K and V of one token and key head
+
     def __init__(self, B: int, Hq: int, Hkv: int, lens: Sequence[int], anchors: Sequence[int],
                  n_layers: int, device, scale: Optional[float] = None):
         if 0 not in anchors:
@@ -52,11 +54,14 @@ class DecodeSchedule:
         self.pooled = torch.zeros(B, Hkv, self.ld, dtype=torch.float32, device=device)
         self.idx = torch.full((B, Hkv, self.k_max), -1, dtype=torch.int32, device=device)
         self.lse = torch.empty(B, Hq, dtype=torch.float32, device=device)
-        wa = api.decode_anchor_workspace_bytes(B, Hq, Hkv, self.max_T)
-        wr = api.decode_reuse_workspace_bytes(B, Hq, Hkv, self.k_max)
-        self.ws = api.workspace(max(wa, wr), device)
-        self.kv_bytes_per_layer = sum(self.lens) * Hkv * self.d * 2 * 2
-        self.reuse_bytes_per_layer = sum(ks) * Hkv * self.d * 2 * 2
+        self.ws = api.workspace(self.workspace_bytes(), device)
+        self.kv_bytes_per_layer = sum(self.lens) * Hkv * self.ROW_BYTES
+        self.reuse_bytes_per_layer = sum(ks) * Hkv * self.ROW_BYTES
+
+    def workspace_bytes(self) -> int:
+        """Scratch of one call, for all layers in turn."""
+        return max(api.decode_anchor_workspace_bytes(self.B, self.Hq, self.Hkv, self.max_T),
+                   api.decode_reuse_workspace_bytes(self.B, self.Hq, self.Hkv, self.k_max))
 
     def is_anchor(self, layer: int) -> bool:
         return layer in self.anchors
@@ -98,7 +103,11 @@ class PagedQ4DecodeSchedule(DecodeSchedule):
     A layer's inputs are a dict of q [B, 1, Hq, 128], k and v [B, 1, Hkv, 128]
     (views into one projection output will do), kv_pages and block_table
     (paging.q4_store), and optionally q_weight and k_weight [128].
+
+    Like its base class a schedule stands at the lengths that it was made with.
     """
+
+    ROW_BYTES = api.Q4_ROW_BYTES
 
     def __init__(self, B: int, Hq: int, Hkv: int, lens: Sequence[int], anchors: Sequence[int],
                  n_layers: int, device, inv_freq: torch.Tensor, dtype=torch.bfloat16, eps: float = 1e-6,
@@ -111,7 +120,9 @@ class PagedQ4DecodeSchedule(DecodeSchedule):
         self.count = torch.tensor([min(T, 1) for T in self.lens], dtype=torch.int32, device=device)
         self.q = torch.empty(B, Hq, 1, self.d, dtype=dtype, device=device)
         self.k = torch.empty(B, Hkv, 1, self.d, dtype=dtype, device=device)
-        self.ws = api.workspace(api.decode_anchor_paged_q4_workspace_bytes(B, Hq, Hkv, self.max_T), device)
+
+    def workspace_bytes(self) -> int:
+        return api.decode_anchor_paged_q4_workspace_bytes(self.B, self.Hq, self.Hkv, self.max_T)
 
     def run_append(self, layer_in: Dict):
         api.qk_norm_rope(layer_in["q"], layer_in["k"], self.positions, self.inv_freq,

@@ -218,6 +218,11 @@ LAUNCHES = {
     "topk": 1,
     "prefill_anchor": 2,  # causal attention (O, LSE), pooled probabilities
     "prefill_reuse": 1,
+    "qk_norm_rope": 1,
+    "kv_write_paged_q4": 1,
+    "kv_read_paged_q4": 1,
+    "decode_anchor_paged_q4": 2,
+    "decode_reuse_paged_q4": 1,
 }
 
 
@@ -226,6 +231,9 @@ def launches_per_step(dec: "DecodeSchedule | None", pre: "PrefillSchedule | None
     for sch, a, r in ((dec, "decode_anchor", "decode_reuse"), (pre, "prefill_anchor", "prefill_reuse")):
         if sch is None:
             continue
+        if isinstance(sch, PagedQ4DecodeSchedule):
+            a, r = a + "_paged_q4", r + "_paged_q4"
+            n += sch.n_layers * (LAUNCHES["qk_norm_rope"] + LAUNCHES["kv_write_paged_q4"])
         for l in range(sch.n_layers):
             n += LAUNCHES[a] + LAUNCHES["topk"] if sch.is_anchor(l) else LAUNCHES[r]
     return n

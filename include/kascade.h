@@ -281,9 +281,12 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
  * Llama-3.1 only the rotation).  For each row x of head_dim channels at position p:
  *   y = x * rsqrt(mean(x^2) + eps) * weight      (y = x where the weight is NULL)
  *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a),  a = p * inv_freq[i], i < 64
- * with j = i + 64, or with channels (2i, 2i+1) when `interleaved` is not 0.  The
- * product p * inv_freq is taken exactly (positions far beyond 2^24 keep their angle),
- * the rest in fp32, and a row is rounded once, when it is stored.
+ * with j = i + 64, or with channels (2i, 2i+1) when `interleaved` is not 0.  The angle
+ * is formed and reduced in fp64, so positions far beyond 2^24 keep it: it is off by at
+ * most |p * inv_freq| * 2^-51 + 2^-22 radians.  The rest is fp32, and a row is rounded
+ * once, when it is stored.  A row whose squares add up to more than the largest float
+ * (bfloat16 elements from 2^60 on) has norm infinity and comes out as 0; with eps = 0
+ * one whose squares vanish (elements below 2^-66) is not finite.
  *
  *   q        bf16, logical [B, N, Hq, 128]: element strides q_strides between sequences,
  *            tokens and heads (multiples of 8, not negative; of no meaning where that
@@ -369,7 +372,10 @@ int kascade_kv_read_paged_q4_f16(kascade_shape s, int32_t N, const uint8_t* kv_p
 
 /* The two decode calls over 4-bit pages: the same operations, outputs, host checks and
  * device-side errors as kascade_decode_anchor_paged and kascade_decode_reuse_paged, on the
- * values the rows stand for.  Logits, softmax statistics and sums are fp32.  A token whose
+ * values the rows stand for.  Logits, softmax statistics and sums are fp32, with weights of
+ * up to 2^8 before they are divided by their sum: K values up to 2^100 and V values up to
+ * 2^116 / T (T tokens of the sequence) are safe from overflow on the way, larger ones may
+ * give infinities or NaN; V groups below 2^-80 in size lose bits.  A token whose
  * block-table entry is out of range gets pooled = 0.  A row that stands for NaN makes its own
  * head group's results NaN.  The reuse call needs no scratch; pooled may be NULL when
  * max_T = 0, and idx when k_max = 0. */

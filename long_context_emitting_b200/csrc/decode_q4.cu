@@ -118,13 +118,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return r;
 }
 
-// Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) that completes on `bar`.
 // Read once: these lines leave L2 first, so that the logits find room there until they are pooled.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+// Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned) that completes on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
                                           uint64_t policy) {
   asm volatile(

@@ -27,17 +27,6 @@ namespace kascade {
 constexpr int kQ4Row = 160;      // bytes of a row
 constexpr int kQ4V = 64;         // byte offset of the V codes
 constexpr int kQ4Tail = 128;     // byte offset of the scales and minima
-constexpr int kQ4Groups = 4;     // scale groups of 32 channels per row
-
-// Byte offset of token t of key head h in a [num_pages, Hkv, page_size, 160]
-// page store, or -1 when its block-table entry is out of range.
-__device__ __forceinline__ int64_t q4_row(const int32_t* table_row, int t, int page_size, int num_pages, int Hkv,
-                                          int h) {
-  const int pi = t / page_size;
-  const int page = __ldg(table_row + pi);
-  if (page < 0 || page >= num_pages) return -1;
-  return (((int64_t)page * Hkv + h) * page_size + (t - pi * page_size)) * kQ4Row;
-}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

@@ -286,7 +286,7 @@ int kascade_decode_reuse_paged_f16(kascade_shape s, const uint16_t* q, const uin
  * most |p * inv_freq| * 2^-51 + 2^-22 radians.  The rest is fp32, and a row is rounded
  * once, when it is stored.  A row whose squares add up to more than the largest float
  * (bfloat16 elements from 2^60 on) has norm infinity and comes out as 0; with eps = 0
- * one whose squares vanish (elements below 2^-66) is not finite.
+ * one whose squares vanish (elements below 2^-66) need not be finite.
  *
  *   q        bf16, logical [B, N, Hq, 128]: element strides q_strides between sequences,
  *            tokens and heads (multiples of 8, not negative; of no meaning where that

@@ -23,9 +23,10 @@
 // two groups into one word.  A block takes 16 tokens (fewer when there are few)
 // through several heads, so that a token's page is looked up once and the next
 // head's rows are on their way while one head's are worked on.
-// Measured on one B200, 26162 tokens x 8 heads in half precision: write 48 us
-// (2.9 TB/s; 320 warp instructions per two rows, so the issue slots, 74% busy,
-// come before memory), read back 28 us (5.0 TB/s).
+// Measured on one B200, 26162 tokens x 8 heads: write 45 us in half precision and 47
+// in bfloat16 (3.0 to 3.1 TB/s; 313 warp instructions per two rows, so the issue
+// slots, 73% busy, come before memory; 64 registers with 8 bytes spilled), read back
+// 28 to 30 us (4.7 to 5.0 TB/s).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "internal.h"

@@ -26,7 +26,7 @@ constexpr unsigned kStatusTimeout = 4u;  // a bounded wait gave up
 // (Giving the attribute to the 16-bit decode anchor's split and combine kernels
 // and to Top-k as well made the 32-layer step 20% slower, so of those only the
 // gather kernel takes it.  The kernels around the 4-bit cache do, through
-// launch_overlapped(): 541 instead of 555 us for a captured step of 8 layers.)
+// launch_overlapped(): 570 instead of 580 us for a captured step of 8 layers.)
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -35,15 +35,17 @@
 //     16 rows of a stage (scores) or the weights' second terms (values).
 //
 // What bounds it, on one B200 (16 sequences of 32K, 32 heads on 8, bfloat16): the
-// first kernel reads 671 MB in 136 to 145 us (by box), 4.6 to 4.9 TB/s; loads and
-// scores alone take 115 us, which is memory.  The rest is the 640 warp instructions
-// per 32 rows, half of them on the half-rate logic pipe to pick nibbles out.  A
-// warp owns a run of rows and a ring of two 32-row stages in shared memory that
+// first kernel reads 671 MB in 144 to 155 us (by box), 4.3 to 4.7 TB/s; loads and
+// scores alone take 115 us, which is memory.  No unit is full beside it (issue
+// slots 62%, logic pipe 56%, tensor pipe 23%): it is the latency of 730 warp
+// instructions per 32 rows at 12 warps per SM, first stall a fixed-latency wait.
+// 168 registers suffice for up to 4 heads; the variants for more spill (anchor 48
+// bytes stored and 68 loaded, reuse 8 and 8).  A warp owns a run of rows and a ring of two 32-row stages in shared memory that
 // bulk copies fill: a half stage is 2560 adjacent bytes.  No registers hold data
 // in flight, and three blocks of four warps per SM leave each thread 168: with
 // four blocks and 128 registers it was 10% slower, with a third stage no faster.
 // A reuse stage is 32 rows of 160 bytes by 16-byte copies, two lanes to a sector;
-// one bulk copy per row took 51 instead of 34 us.  Rows lie 160 bytes apart, which is
+// one bulk copy per row took half as long again.  Rows lie 160 bytes apart, which is
 // 8 banks mod 32; the fragment rows are taken in the order 0 6 1 7 2 4 3 5 so
 // that the 16-byte K reads (pairs of rows) and the 8-byte V reads (every second
 // fragment row) both meet different banks.
@@ -134,9 +136,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Asynchronous copy of 16 bytes (zeros where src_bytes is 0).  The 64-byte hint matters: a row is 160
-// bytes, and without it whole 128-byte lines came from memory, 256 bytes a row instead of 192
-// (105 against 80 MB for 16 sequences of 32K, 26.6 against 24.8 us).
+// Asynchronous copy of 16 bytes (zeros where src_bytes is 0).  The 64-byte hint is for rows of 160 bytes:
+// without it whole 128-byte lines come from memory, 256 bytes a row instead of 192 (105 against 80 MB for
+// 16 sequences of 32K; 26.6 against 26.2 us, ragged 44.45 against 44.15).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::64B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
                "r"(src_bytes), "l"(policy)
@@ -497,7 +499,9 @@ __device__ __forceinline__ void values(State& w, uint32_t rows, int gid, int tig
 // merging a unit costs a block about as much as kUnitCost stages, so a unit is that much longer on
 // the line.  A block's part of unit u goes to slot block + u of the partial results: both only ever
 // grow along the line, so no two parts meet, and a unit's slots follow one another.
-constexpr int kUnitCost = 12;  // a ragged batch: 52 us with 4, 43 with 8, 42 with 16
+// Measured with 4, 8, 12, 16 and 24: 65536 ... 0 tokens (8 sequences, 8 heads, half) 50.1, 34.8, 33.2, 33.2, 33.5 us;
+// one of 64K beside 31 of 300 45.7, 42.4, 43.2, 44.2, 46.4; 64 of 200 to 2153 48.3, 45.9, 46.1, 46.7, 48.1.
+constexpr int kUnitCost = 12;
 __device__ __forceinline__ int stages_of(int T, int max_T) {
   return T > 0 && T <= max_T ? (T + kStageRows - 1) / kStageRows : 0;
 }

@@ -265,15 +265,22 @@ def _whole(name: str, t, dtype: torch.dtype, dev: int) -> int:
     return t.data_ptr()
 
 
+def _rows_lie(t: torch.Tensor, inner: tuple) -> bool:
+    """Whether the start of a contiguous tensor reads as rows of ``inner`` one after the other: its
+    dimensions after the first are the last ones of ``inner``, or none (those of length 1 aside)."""
+    have, want = [x for x in t.shape[1:] if x != 1], [x for x in inner if x != 1]
+    return have == want[len(want) - len(have):]
+
+
 def _sized(name: str, t, dtype: torch.dtype, n: int, dev: int, inner: tuple = ()) -> int:
     """The address of a tensor on device ``dev`` whose first ``n`` elements are what the call wants: a
-    contiguous one of that size, or a longer one whose dimensions after the first are ``inner``
-    (buffers for more sequences), so that its rows lie where the call looks for them."""
+    contiguous one of that size, or a longer one (a buffer for more sequences) whose rows of
+    ``inner`` lie where the call looks for them."""
     if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.numel() == n
             and t.is_contiguous()):
         _need_size(name, t, dtype, n)
         _need_device(name, t, dev)
-        if t.numel() > n and t.dim() > 1 and tuple(t.shape[1:]) != inner:
+        if t.numel() > n and not _rows_lie(t, inner):
             raise ValueError(f"{name} is {list(t.shape)}; a longer buffer than {n} elements must be {['...', *inner]}")
     return t.data_ptr()
 
@@ -406,7 +413,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: f
     qp, qs = _rows("q", q, dt, (B, N, Hq, d), dev)
     kp, ks = _rows("k", k, dt, (B, N, Hkv, d), dev)
     pos = _sized("positions", positions, torch.int32, B * N, dev, (N,))
-    if N > 1 and positions.dim() > 1 and positions.shape[-1] != N:
+    if N > 1 and positions.dim() > 1 and not _rows_lie(positions, (N,)):
         raise ValueError(f"positions must be [{B}, {N}], got {list(positions.shape)}")
     inv = _exactly("inv_freq", inv_freq, torch.float32, HEAD_DIM // 2, dev)
     qw = None if q_weight is None else _exactly("q_weight", q_weight, dt, d, dev)

@@ -64,3 +64,34 @@ def test_attention_layouts(fake):  # noqa: F811
     for kw in (dict(idx=_i32(2, 4, 7)), dict(ik=_i32(2, 4)), dict(hm=_i32(2, 2))):
         with pytest.raises(ValueError):
             reuse(**kw)
+
+
+def test_rows_lie_where_memory_says_so():
+    """Against the places of the elements themselves: a longer buffer is taken only if the call's rows start it."""
+    import itertools
+
+    for inner in ((), (3,), (2, 3), (2, 1, 4)):
+        rows = 1
+        for x in inner:
+            rows *= x
+        for n in range(1, 4):
+            for shape in itertools.product(range(1, 6), repeat=n):
+                t = torch.empty(shape)
+                if api._rows_lie(t, inner):
+                    # the dimensions after the first split a row of `inner`, or are one
+                    rest = t[0].numel()
+                    assert rows % rest == 0
+    for t, inner, ok in ((_i32(5, 1), (), True), (_i32(5, 2), (), False), (_i32(8, 7), (2, 7), True),
+                         (_i32(3, 2, 7), (2, 7), True), (_i32(3, 4, 7), (2, 7), False), (_i32(3, 7, 2), (2, 7), False),
+                         (_i32(3, 2), (2, 7), False), (_i32(9), (2, 7), True), (_i32(4, 3, 1), (3,), True)):
+        assert api._rows_lie(t, inner) == ok, (t.shape, inner)
+
+
+def test_harmless_longer_buffers_are_taken(fake):  # noqa: F811
+    q, k = _bf(2, 3, 8, 128), _bf(2, 3, 2, 128)
+    api.qk_norm_rope(q, k, _i32(2, 3, 1), torch.zeros(1, 64))
+    pages, table = paging.q4_store([40, 1], 2, 16, "cpu")
+    api.kv_read_paged_q4(pages, table, 16, _i32(2), _i32(5, 1), 5, k=_bf(99, 128))
+    q, sl = _bf(2, 8, 128), _i32(4, 1)
+    api.decode_anchor_paged_q4(q, pages, table, 16, sl, 40, 0.1, 2, pooled=torch.zeros(9, 40))
+    api.decode_reuse_paged_q4(q, pages, table, 16, sl, _i32(9, 7), _i32(7, 1), _i32(3, 1), 0.1, 2)

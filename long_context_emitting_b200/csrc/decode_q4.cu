@@ -29,8 +29,8 @@
 //     sums stay.  The minima are summed in fp32 (8 sums per lane).
 //   * The running maximum moves only when a score exceeds it by 8 (weights then
 //     reach 2^8 instead of 1), so most stages need one vote instead of a
-//     reduction and a rescale of the sums.  Values up to 2^100 are safe from
-//     overflow on the way.
+//     reduction and a rescale of the sums.  V up to 2^116 / T and K up to 2^100 are
+//     safe from overflow on the way.
 //   * Up to 4 heads fill half the columns.  The other half then serves the second
 //     16 rows of a stage (scores) or the weights' second terms (values).
 //
@@ -40,10 +40,11 @@
 // slots 62%, logic pipe 56%, tensor pipe 23%): it is the latency of 730 warp
 // instructions per 32 rows at 12 warps per SM, first stall a fixed-latency wait.
 // 168 registers suffice for up to 4 heads; the variants for more spill (anchor 48
-// bytes stored and 68 loaded, reuse 8 and 8).  A warp owns a run of rows and a ring of two 32-row stages in shared memory that
-// bulk copies fill: a half stage is 2560 adjacent bytes.  No registers hold data
-// in flight, and three blocks of four warps per SM leave each thread 168: with
-// four blocks and 128 registers it was 10% slower, with a third stage no faster.
+// bytes stored and 68 loaded, reuse 8 and 8).  A warp owns a run of rows and a ring
+// of two 32-row stages in shared memory that bulk copies fill: a half stage is 2560
+// adjacent bytes.  No registers hold data in flight, and three blocks of four warps
+// per SM leave each thread 168: with four blocks and 128 registers it was 10%
+// slower, with a third stage no faster.
 // A reuse stage is 32 rows of 160 bytes by 16-byte copies, two lanes to a sector;
 // one bulk copy per row took half as long again.  Rows lie 160 bytes apart, which is
 // 8 banks mod 32; the fragment rows are taken in the order 0 6 1 7 2 4 3 5 so
